@@ -286,6 +286,136 @@ DF2_API df2_status dflash2_dynamic_conv(const df2_conv_dims *dims, const void *x
                                         const void *base, const float *dyn, const void *gamma, float eps, void *y,
                                         void *stream);
 
+/* ==== attention of the drafter's layers: rotary positions, the paged cache, attention over it ====
+ *
+ * The blocks whose hidden states the selector head scores come out of attention layers: a
+ * block of new tokens (a draft block, the tokens a target verifies, a prompt's chunk) is
+ * rotated by its positions, its keys and values are written into a paged cache, and its
+ * queries attend over that cache.  ("DFlash2 Lands in llama.cpp", the layer order in "Dynamic
+ * Local Convolution"; the pages give the attention no formula of its own: these are the usual ones.)
+ * None of these calls synchronises or allocates; each is captured into a CUDA graph as it is.
+ */
+
+/* bf16 rows [N tokens, heads, dim]: element d of head h of token n is
+ * data[n * token_stride + h * head_stride + d].  Strides count elements and are multiples of 8;
+ * data is 16-byte aligned.  Views of a fused q | k | v projection are given as they are. */
+typedef struct df2_heads {
+    void *data;
+    int32_t heads;
+    int64_t token_stride, head_stride;
+} df2_heads;
+
+/* Rotary positions: a table of cosines and sines, float [max_pos, 2, rot / 2] (cosines of a
+ * position, then its sines; dflash2_rope_table makes one), 4-byte aligned.  The first `rot`
+ * elements of a head turn in pairs and the rest pass through: with interleaved == 0 element i
+ * pairs with i + rot/2, otherwise 2i with 2i+1, and for pair i
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i).
+ * Products and sums are rounded separately in float32; the result once to its type.
+ * Positions outside [0, max_pos) are clamped into it. */
+typedef struct df2_rope {
+    const float *table;
+    int32_t max_pos, rot, interleaved;
+} df2_rope;
+
+typedef enum df2_rope_kind {
+    DF2_ROPE_PLAIN = 0,  /* f_i = theta^(-2i/rot)                                                       */
+    DF2_ROPE_LINEAR = 1, /* f_i / factor                                                                */
+    DF2_ROPE_BASE = 2,   /* theta * factor^(rot/(rot-2)) in theta's place                               */
+    DF2_ROPE_RAMP = 3,   /* f_i for pairs that turn over `high` times within original_len, f_i / factor
+                            for those that turn under `low` times, a linear ramp over the pair index
+                            between them (its ends rounded outwards); tables times `multiplier`         */
+    DF2_ROPE_BAND = 4    /* f_i where original_len / wavelength >= high, f_i / factor where it is
+                            <= low, linear in original_len / wavelength between them                    */
+} df2_rope_kind;
+
+typedef struct df2_rope_scaling {
+    int32_t kind; /* df2_rope_kind */
+    double theta, factor, original_len, low, high, multiplier;
+} df2_rope_scaling;
+
+/* Fills a table float [max_pos, 2, rot / 2]; frequencies, angles, cosines and sines are
+ * computed in double and rounded once.  rot even, 2 <= rot <= 256; theta > 1, factor > 0 and
+ * multiplier > 0; for RAMP and BAND original_len > 0 and 0 < low < high; finite throughout. */
+DF2_API df2_status dflash2_rope_table(const df2_rope_scaling *scaling, int32_t max_pos, int32_t rot, float *table,
+                                      void *stream);
+
+/* y = x [N, heads, dim] rotated by positions int32 [N]; inverse != 0 turns the other way, which
+ * is the gradient of the forward rotation (given dL/dy it makes dL/dx).  y may be x itself (the
+ * same strides); otherwise the two must not overlap.  dim a multiple of 8 up to 256, rot <= dim. */
+DF2_API df2_status dflash2_rope(const df2_rope *rope, int32_t N, int32_t dim, const df2_heads *x,
+                                const int32_t *positions, int32_t inverse, const df2_heads *y, void *stream);
+
+typedef enum df2_cache_type { DF2_CACHE_BF16 = 0, DF2_CACHE_E4M3 = 1, DF2_CACHE_INT8 = 2 } df2_cache_type;
+
+/* One layer's paged cache: k and v [pages, heads, page_size, dim] of the type (16-byte
+ * aligned), and for the 8-bit types k_scale and v_scale float [pages, heads, page_size] (4-byte
+ * aligned; NULL for bf16).  A row (one token, one head) is held as codes times its scale:
+ *   m = max |row|,  scale = m / M,  code = round(row * (M / m)),  M = 448 (e4m3) or 127 (int8),
+ * each operation in float32, codes rounded to nearest even.  A row with m < 1e-30 is held as
+ * zeros; one that is not finite gets a NaN scale and reads back as NaN throughout.
+ * page_size a multiple of 8 up to 1024; dim a multiple of 16 up to 128; 1 <= heads <= 1024. */
+typedef struct df2_cache {
+    int32_t pages, page_size, heads, dim, type;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} df2_cache;
+
+/* The new tokens of B sequences, packed: sequence b has the n_b = token_start[b+1] -
+ * token_start[b] rows from token_start[b] on.  They are the last n_b of the kv_len[b] tokens
+ * that the cache holds of it (counting them): row i is at position kv_len[b] - n_b + i, which
+ * lives in page page_table[b, position / page_size].  All three are device arrays.
+ *   token_start int32 [B + 1], rising from 0 to N;  kv_len int32 [B];
+ *   page_table int32 [B, max_pages]: only the entries of positions that a call touches are used.
+ * max_new: no n_b is larger.  A row whose position is negative (kv_len[b] < n_b) is padding: it
+ * is not written, reads back as zeros, and with causal attention sees nothing.  Page ids outside
+ * [0, pages) and positions past max_pages * page_size are the caller's mistake: they are not
+ * written, read back as zeros and are attended to with unspecified results, but no access
+ * leaves the tensors.  The attention calls take kv_len as at most max_pages * page_size. */
+typedef struct df2_tokens {
+    int32_t B, N, max_new, max_pages;
+    const int32_t *token_start, *kv_len, *page_table;
+} df2_tokens;
+
+/* Writes the new tokens' keys and values into the cache, keys (and queries) rotated first.
+ *   rope   or NULL: nothing is rotated          k, v  bf16 [N, cache heads, dim]
+ *   q, q_out  bf16 [N, q heads, dim], both or neither (NULL): q_out = rotated q (may be q itself)
+ * One launch.  Rotation and quantisation in float32, no rounding between them. */
+DF2_API df2_status dflash2_cache_append(const df2_cache *cache, const df2_tokens *tokens, const df2_rope *rope,
+                                        const df2_heads *q, const df2_heads *q_out, const df2_heads *k,
+                                        const df2_heads *v, void *stream);
+
+/* Reads the tokens' rows back: k_out, v_out bf16 [N, cache heads, dim], code * scale rounded
+ * once (NULL for either skips it).  With n_b = kv_len[b] that is the whole of each sequence. */
+DF2_API df2_status dflash2_cache_read(const df2_cache *cache, const df2_tokens *tokens, const df2_heads *k_out,
+                                      const df2_heads *v_out, void *stream);
+
+/* Row i of sequence b, at position p = kv_len[b] - n_b + i, sees the positions j with
+ *   0 <= j < kv_len[b],  j <= p if causal,  j > p - window if window > 0. */
+typedef struct df2_attention {
+    float scale;    /* of the scores; finite */
+    int32_t causal; /* 0: every new token sees all the others (a draft block) */
+    int32_t window; /* 0: no limit */
+} df2_attention;
+
+/* Bytes of workspace of dflash2_paged_attention (0 if the arguments are out of limits), for the
+ * current device.  It begins with a status word that must be zero before the first call
+ * (dflash2_check_device_status reads and clears it); the rest needs no initialisation.  One
+ * workspace serves one stream at a time. */
+DF2_API size_t dflash2_paged_attention_workspace_bytes(const df2_cache *cache, const df2_tokens *tokens,
+                                                       int32_t q_heads);
+
+/* out [N, q heads, dim] bf16 = softmax(scale * q . K) . V over what each row sees in the cache
+ * (the new tokens' own rows included: append them first), query head h on cache head
+ * h / (q heads / cache heads).  lse float [N, q heads] or NULL: the natural logarithm of the sum
+ * of the exponentials.  A row that sees nothing gets zeros and -inf.
+ * What the cache and the page table hold for positions that no row of a sequence sees may be
+ * anything (a last page's tail, pages given back below a window).  A key that is not finite
+ * reaches the rows that see it; a value that is not finite may reach every row of its sequence.
+ * q heads a multiple of cache heads, at most 64 times as many; B <= 4096; N * q heads < 2^31. */
+DF2_API df2_status dflash2_paged_attention(const df2_cache *cache, const df2_tokens *tokens,
+                                           const df2_attention *options, const df2_heads *q, const df2_heads *out,
+                                           float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, reads and clears the sticky device status word in `workspace`.
  * Returns DF2_ERR_TIMEOUT if a pipeline wait inside any kernel gave up since the last
  * check (the kernel then skipped its remaining work and its outputs are invalid). */

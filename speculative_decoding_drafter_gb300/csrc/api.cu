@@ -7,22 +7,11 @@
 #include <cstdint>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_common.h"
 #include "dflash2.h"
 #include "internal.h"
 
 namespace df2 {
-
-// NVTX range around an entry point: the calls show up by name in a profiler's timeline, and
-// `ncu --nvtx --nvtx-include "dflash2_select/"` captures the kernels of one call.  Without a
-// profiler attached the push and pop return at once (header-only NVTX, no library linked).
-struct TraceRange {
-    explicit TraceRange(const char *name) { nvtxRangePushA(name); }
-    ~TraceRange() { nvtxRangePop(); }
-    TraceRange(const TraceRange &) = delete;
-    TraceRange &operator=(const TraceRange &) = delete;
-};
 
 int device_sm_count()
 {
@@ -67,12 +56,6 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
 }
 
 namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 df2_status check_dims(const df2_dims *d)
 {
@@ -178,22 +161,11 @@ df2_status check_workspace(const df2_dims &d, void *ws, size_t bytes)
     return DF2_OK;
 }
 
-df2_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DF2_OK : DF2_ERR_CUDA; }
-
 // Events recorded around the top-k producing launch (dflash2_profile_events).
 thread_local cudaEvent_t t_profile_begin = nullptr;
 thread_local cudaEvent_t t_profile_end = nullptr;
 
 cudaError_t profile_mark(cudaEvent_t ev, cudaStream_t st) { return ev ? cudaEventRecord(ev, st) : cudaSuccess; }
-
-#define DF2_TRY(expr)                        \
-    do {                                     \
-        const df2_status _s = (expr);        \
-        if (_s != DF2_OK)                    \
-            return _s;                       \
-    } while (0)
-
-#define DF2_CUDA(expr) DF2_TRY(from_cuda(expr))
 
 // Shared tail of both select paths: merge, lattice and walk in one launch.
 df2_status finish(const df2_dims &d, const Workspace &w, int n_split, const float *gate, const void *pred_cb,

@@ -123,6 +123,63 @@ cudaError_t launch_dynamic_conv(int B, int T, int C, int G, const uint16_t *x, c
 // Greedy walk, one warp per sequence: draft_ids [B, T].
 cudaError_t launch_walk(int B, int T, int k, const float *lattice, int32_t *draft_ids, cudaStream_t stream);
 
+// ---- attention of the drafter's layers (layouts and limits: dflash2.h)
+
+// bf16 rows [N, heads, dim] with strides in elements.
+struct HeadRows {
+    uint16_t *data = nullptr;
+    int heads = 0;
+    long long token_stride = 0, head_stride = 0;
+};
+
+struct RopeTable {
+    const float *table = nullptr;  // null: no rotation
+    int max_pos = 0, rot = 0, interleaved = 0;
+};
+
+struct PagedCache {
+    int pages = 0, page_size = 0, heads = 0, dim = 0, type = 0;
+    void *k = nullptr, *v = nullptr;
+    float *k_scale = nullptr, *v_scale = nullptr;
+};
+
+struct TokenBatch {
+    int B = 0, N = 0, max_new = 0, max_pages = 0;
+    const int32_t *token_start = nullptr, *kv_len = nullptr, *page_table = nullptr;
+};
+
+struct RopeScaling {
+    int kind;
+    double theta, factor, original_len, low, high, multiplier;
+};
+
+struct AttentionOptions {
+    float scale = 1.f;
+    int causal = 1, window = 0;
+};
+
+cudaError_t launch_rope_table(const RopeScaling &s, int max_pos, int rot, float *table, cudaStream_t stream);
+
+// y = x rotated by positions [N] (sine_sign -1: the other way).
+cudaError_t launch_rope(const RopeTable &rope, int N, int dim, const HeadRows &x, const int32_t *positions,
+                        float sine_sign, const HeadRows &y, cudaStream_t stream);
+
+// Rotates q (if any) and k, writes k and v into the cache.
+cudaError_t launch_cache_append(const PagedCache &cache, const TokenBatch &tokens, const RopeTable &rope,
+                                const HeadRows &q, const HeadRows &q_out, const HeadRows &k, const HeadRows &v,
+                                cudaStream_t stream);
+
+// The tokens' rows as bf16; k_out or v_out may have null data.
+cudaError_t launch_cache_read(const PagedCache &cache, const TokenBatch &tokens, const HeadRows &k_out,
+                              const HeadRows &v_out, cudaStream_t stream);
+
+// Bytes of scratch behind the status word.
+size_t paged_attention_scratch(const PagedCache &cache, const TokenBatch &tokens, int q_heads);
+
+cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &tokens, const AttentionOptions &opt,
+                                   const HeadRows &q, const HeadRows &out, float *lse, uint32_t *status,
+                                   void *scratch, cudaStream_t stream);
+
 // Launches `kernel` as a programmatic dependent of the kernel before it on `stream`: it may
 // start under that kernel's tail, and must wait for it (griddep_wait in every CTA, before
 // anything it reads or writes) so that its own completion still implies that kernel's.

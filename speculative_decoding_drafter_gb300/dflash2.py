@@ -33,6 +33,8 @@ EXPORTED_SYMBOLS = (
     "dflash2_check_device_status", "dflash2_status_string", "dflash2_version", "dflash2_profile_events",
     "dflash2_topk_noalloc", "dflash2_walk_sample", "dflash2_dynamic_conv", "dflash2_select_host",
     "dflash2_select_host_workspace_bytes", "dflash2_selftest_wait_timeout", "dflash2_select_walk",
+    "dflash2_rope_table", "dflash2_rope", "dflash2_cache_append", "dflash2_cache_read",
+    "dflash2_paged_attention_workspace_bytes", "dflash2_paged_attention",
 )
 
 
@@ -50,6 +52,39 @@ class WalkOpts(ctypes.Structure):
     """df2_walk_opts: temperature, p_min, uniforms [B, T] (or NULL: greedy), n_draft [B], confidence [B, T]."""
     _fields_ = [("temperature", ctypes.c_float), ("p_min", ctypes.c_float), ("uniforms", ctypes.c_void_p),
                 ("n_draft", ctypes.c_void_p), ("confidence", ctypes.c_void_p)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("multiplier", ctypes.c_double)]
+
+
+class HeadRows(ctypes.Structure):
+    """df2_heads: bf16 rows [N, heads, dim] with strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int32), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("rot", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("type", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class TokenArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("N", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("token_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("causal", ctypes.c_int32), ("window", ctypes.c_int32)]
 
 
 class Dims(ctypes.Structure):
@@ -96,6 +131,18 @@ def library(path: str | None = None):
                 "dflash2_select_host": (I, [D, P, P, P, P, P, P, P, P, P, P, S, P]),
                 "dflash2_select_host_workspace_bytes": (S, [D]),
                 "dflash2_selftest_wait_timeout": (I, [ctypes.c_uint32, P, S, P]),
+                "dflash2_rope_table": (I, [ctypes.POINTER(RopeScaling), ctypes.c_int32, ctypes.c_int32, P, P]),
+                "dflash2_rope": (I, [ctypes.POINTER(RopeArgs), ctypes.c_int32, ctypes.c_int32,
+                                     ctypes.POINTER(HeadRows), P, ctypes.c_int32, ctypes.POINTER(HeadRows), P]),
+                "dflash2_cache_append": (I, [ctypes.POINTER(CacheArgs), ctypes.POINTER(TokenArgs),
+                                             ctypes.POINTER(RopeArgs), *[ctypes.POINTER(HeadRows)] * 4, P]),
+                "dflash2_cache_read": (I, [ctypes.POINTER(CacheArgs), ctypes.POINTER(TokenArgs),
+                                           *[ctypes.POINTER(HeadRows)] * 2, P]),
+                "dflash2_paged_attention_workspace_bytes": (S, [ctypes.POINTER(CacheArgs), ctypes.POINTER(TokenArgs),
+                                                                ctypes.c_int32]),
+                "dflash2_paged_attention": (I, [ctypes.POINTER(CacheArgs), ctypes.POINTER(TokenArgs),
+                                                ctypes.POINTER(AttentionArgs), *[ctypes.POINTER(HeadRows)] * 2, P, P,
+                                                S, P]),
                 "dflash2_select_walk": (I, [D, ctypes.POINTER(WalkOpts), P, P, P, P, P, P, P, P, P, P, P, P, S, P]),
             }
             for name, (res, args) in sig.items():
