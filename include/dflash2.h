@@ -366,7 +366,7 @@ typedef struct df2_cache {
  * lives in page page_table[b, position / page_size].  All three are device arrays.
  *   token_start int32 [B + 1], rising from 0 to N;  kv_len int32 [B];
  *   page_table int32 [B, max_pages]: only the entries of positions that a call touches are used.
- * max_new: no n_b is larger.  A row whose position is negative (kv_len[b] < n_b) is padding: it
+ * max_new: no n_b is larger.  B <= 2048.  A row whose position is negative (kv_len[b] < n_b) is padding: it
  * is not written, reads back as zeros, and with causal attention sees nothing.  Page ids outside
  * [0, pages) and positions past max_pages * page_size are the caller's mistake: they are not
  * written, read back as zeros and are attended to with unspecified results, but no access
@@ -411,7 +411,7 @@ DF2_API size_t dflash2_paged_attention_workspace_bytes(const df2_cache *cache, c
  * What the cache and the page table hold for positions that no row of a sequence sees may be
  * anything (a last page's tail, pages given back below a window).  A key that is not finite
  * reaches the rows that see it; a value that is not finite may reach every row of its sequence.
- * q heads a multiple of cache heads, at most 64 times as many; B <= 4096; N * q heads < 2^31. */
+ * q heads a multiple of cache heads, at most 64 times as many; N * q heads < 2^31. */
 DF2_API df2_status dflash2_paged_attention(const df2_cache *cache, const df2_tokens *tokens,
                                            const df2_attention *options, const df2_heads *q, const df2_heads *out,
                                            float *lse, void *workspace, size_t workspace_bytes, void *stream);

@@ -88,7 +88,7 @@ df2_status check_tokens_limits(const df2_tokens *t)
     if (!t || t->B < 1 || t->N < 0 || t->max_new < 0 || t->max_new > t->N || t->max_pages < 0 ||
         (t->N > 0 && t->max_new < 1))
         return DF2_ERR_INVALID_ARG;
-    if (t->B > 4096)
+    if (t->B > 2048)
         return DF2_ERR_UNSUPPORTED;
     return DF2_OK;
 }

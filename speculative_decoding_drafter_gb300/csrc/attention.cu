@@ -1,139 +1,1183 @@
-// attention.cu -- attention of a block of new tokens over the paged cache.
+// attention.cu -- attention of a block of new tokens over the paged cache, on tcgen05 tensor cores.
 //
-// The plain kernel: one warp a row (token, query head), 32 keys at a time, each lane the score of
-// one key, with the running maximum m and sum l of the softmax:
-//   m' = max(m, s_j), l' = l 2^(m - m') + sum 2^(s_j - m'), o' = o 2^(m - m') + sum 2^(s_j - m') v_j
-// (scores in units of log 2), then each lane four dimensions of o over the 32 values.
+// For query row r (a token and a query head) over the keys j it sees:
+//   x_j = scale log2(e) q_r . k_j,   m = max x_j,   l = sum 2^(x_j - m),   o = sum 2^(x_j - m) v_j / l
+// in one pass over tiles of 128 keys with a running m: when a tile raises it, l and o are scaled by
+// 2^(m_old - m_new).  As long as it rises by no more than 8 (a factor 256, harmless in float32 and
+// in the 16-bit probabilities) the old m is kept, so o is seldom touched.
+//
+// A work item is a sequence, a cache head and a run of its new tokens: the query heads that share
+// the cache head are rows of the same tile (token major), 128 rows a tile, one or two tiles.
+// Each CTA (one per SM) takes an equal share of all (item, key tile) pairs in order; an item that
+// crosses a border is finished by the combine kernel from partial (o, m, l).
+//
+// Roles of a CTA: warp 0 loads K and V tiles by TMA, a box per run of a page; one thread of warp 1
+// issues the MMAs; a warpgroup per row tile does the softmax, a thread per row, S read from and P
+// written back to tensor memory; with an 8-bit cache one more warpgroup widens the codes to f16.
+//   S = Q K^T   both K-major from shared memory          D[128 x 128] in TMEM
+//   O += P V    P from TMEM over S, V as it lies (its rows are the K dimension: MN-major B)
+// 8-bit caches: codes are exact in f16, so K's scale multiplies the score, and V's goes into the
+// exponent: x'_j = x_j + log2(vs_j), P'_j = 2^(x'_j - m'), o = sum P'_j code_j, l = sum P'_j / vs_j,
+// which keeps P' in f16's range whatever the values' size.  Queries go to f16 by a power of two per
+// row that brings the row's largest magnitude to 2^14..2^15 (smaller parts lose bits only below
+// 2^-24 of it).  With a bf16 cache everything stays bf16; P is rounded once, to bf16 or f16.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "internal.h"
 #include "paged.cuh"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace df2 {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int BM = 128;  // rows of a tile
+constexpr int BN = 128;  // keys of a tile
+constexpr int HALF_BYTES = 128 * 128;  // 128 rows of 64 16-bit elements
+constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr int MAX_RING = 8;
+constexpr int WIDE_RING = 3;  // widened 8-bit tiles
+constexpr float kLeastScale = -108.f;  // log2 of the least scale a cache holds, 1e-30 / 448
+constexpr float LAZY = 8.f;   // how far the running maximum may lag, in powers of two
 
-struct AttnArgs {
+struct SplitRecord {  // an item whose pieces the combine kernel joins
+    int32_t valid, first_slot, c0, c1, kvh, tok0, ntok, pad;
+};
+
+struct Args {
     PagedCache cache;
     TokenBatch tokens;
     HeadRows q, out;
     float *lse;
     float scale_log2;
+    uint32_t q_and, q_xor;  // scale 0 clears q, a negative one flips its sign
     int causal, window, group;
+    int tpm;   // tokens of a row tile
+    int span;  // tokens of an item
+    int box;   // rows of a TMA box: gcd(page_size, 128)
+    int ring;  // stages of the TMA ring
+    SplitRecord *records;
+    float2 *part_ml;  // [2 * grid][rows]: (maximum in powers of two, sum)
+    float *part_o;    // [2 * grid][rows][dim]
+    uint32_t *status;
 };
 
-// Element d of cached row `row`, without its scale.
-__device__ __forceinline__ float code_at(const PagedCache &c, const void *base, long long row, int d)
+struct Sequence {
+    int start, n, len;
+};
+
+__device__ __forceinline__ Sequence sequence_at(const Args &a, int b)
 {
-    const long long at = row * c.dim + d;
-    if (c.type == 0)
-        return bf16_lo(static_cast<const uint16_t *>(base)[at]);
-    if (c.type == 2)
-        return static_cast<const int8_t *>(base)[at];
-    uint32_t w;
-    float f;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"(static_cast<uint16_t>(static_cast<const uint8_t *>(base)[at])));
-    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(f) : "r"(w));
-    return f;
+    Sequence s;
+    s.start = min(max(__ldg(a.tokens.token_start + b), 0), a.tokens.N);
+    s.n = min(max(__ldg(a.tokens.token_start + b + 1), s.start), a.tokens.N) - s.start;
+    s.len = min(max(__ldg(a.tokens.kv_len + b), 0), a.tokens.max_pages * a.cache.page_size);
+    return s;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) attention_kernel(const AttnArgs a)
+struct Item {
+    int tok0, ntok;    // first token in its sequence, tokens
+    int p0;            // position of the first
+    int lo, hi;        // positions some row sees
+    int tile0, tiles;  // key tiles (one, empty, if nothing is seen)
+};
+
+__device__ __forceinline__ Item item_at(const Args &a, const Sequence &s, int qt)
 {
-    __shared__ float qs[kWarps][128];
+    Item it;
+    it.tok0 = qt * a.span;
+    it.ntok = min(s.n - it.tok0, a.span);
+    it.p0 = s.len - s.n + it.tok0;
+    it.hi = a.causal ? min(s.len, it.p0 + it.ntok) : s.len;
+    it.lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
+    if (it.hi <= it.lo) {
+        it.lo = it.hi = it.tile0 = 0;
+        it.tiles = 1;
+    } else {
+        it.tile0 = it.lo / BN;
+        it.tiles = (it.hi - 1) / BN - it.tile0 + 1;
+    }
+    return it;
+}
+
+__device__ __forceinline__ int items_of(const Args &a, const Sequence &s) { return (s.n + a.span - 1) / a.span; }
+
+// A run of key tiles of one item.
+struct Segment {
+    Item item;
+    int b, kvh, start;   // start: the sequence's first packed token
+    int tile, tiles;
+    long long u;         // units before it
+    bool first, last;    // has the item's first / last tile
+};
+
+// The segments of a CTA's share [u, u_end) of the units (cache head by cache head, item by item).
+struct Walk {
+    long long u, u_end;
+    int b, kvh, qt, off, nq;
+    Sequence s;
+
+    __device__ __forceinline__ void begin(const Args &a, const int *prefix, long long units, int grid, int c)
+    {
+        u = c * units / grid;
+        u_end = (c + 1) * units / grid;
+        int lo = 0, hi = a.tokens.B;  // the largest b with prefix[b] * heads <= u
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (static_cast<long long>(prefix[mid]) * a.cache.heads <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        b = lo;
+        s = sequence_at(a, b);
+        nq = items_of(a, s);
+        const int per_head = max(prefix[b + 1] - prefix[b], 1);
+        const int r = static_cast<int>(u - static_cast<long long>(prefix[b]) * a.cache.heads);
+        kvh = r / per_head;
+        off = r - kvh * per_head;
+        for (qt = 0; qt + 1 < nq; ++qt) {
+            const int t = item_at(a, s, qt).tiles;
+            if (off < t)
+                break;
+            off -= t;
+        }
+    }
+
+    __device__ __forceinline__ bool next(const Args &a, Segment &g)
+    {
+        if (u >= u_end)
+            return false;
+        while (kvh == a.cache.heads) {  // the next sequence that has tokens
+            ++b;
+            s = sequence_at(a, b);
+            nq = items_of(a, s);
+            kvh = nq > 0 ? 0 : a.cache.heads;
+        }
+        g.item = item_at(a, s, qt);
+        g.b = b;
+        g.kvh = kvh;
+        g.start = s.start;
+        g.u = u;
+        g.tile = g.item.tile0 + off;
+        g.tiles = static_cast<int>(min(static_cast<long long>(g.item.tiles - off), u_end - u));
+        g.first = off == 0;
+        u += g.tiles;
+        off += g.tiles;
+        g.last = off == g.item.tiles;
+        if (g.last) {
+            off = 0;
+            if (++qt == nq) {
+                qt = 0;
+                ++kvh;
+            }
+        }
+        return true;
+    }
+};
+
+// Position in a ring of `size` slots, two items (a K and a V) at a time.
+struct RingAt {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void step(int size)
+    {
+        slot += 2;
+        if (slot >= size) {
+            slot -= size;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t f16_pack(float a, float b)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+
+// Four codes of an 8-bit cache as f16 (exact).
+template <int TYPE>
+__device__ __forceinline__ uint2 widen4(uint32_t w)
+{
+    uint2 r;
+    if constexpr (TYPE == 1) {
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.x) : "h"(static_cast<uint16_t>(w)));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r.y) : "h"(static_cast<uint16_t>(w >> 16)));
+    } else {
+        // 0x6400 | u is the f16 number 1024 + u; u = code + 128
+        w ^= 0x80808080u;
+        const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.x) : "r"(lo), "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r.y) : "r"(hi), "r"(0x64806480u));
+    }
+    return r;
+}
+
+template <int QT, int TYPE>
+struct Shape {
+    static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 1 : 0));
+    // registers of a thread after the roles part: control, softmax, widening (their sum times 128
+    // is at most what the launch holds: 65536 / threads, a multiple of 8, times the threads)
+    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 184 : 216;
+    static constexpr int kWideRegs = QT == 2 ? 80 : 160;
+    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 64 : 128;
+    static constexpr bool kSplitRegs = kThreads > 256;
+};
+
+// A softmax warp's walk, kept in shared memory: its registers hold a row of scores.
+struct WarpWalk {
+    Walk walk;
+    Segment seg[2];
+    int have[2];
+};
+
+// Shared memory: Q tiles | TMA ring | widened ring (8-bit) | scales (8-bit) | barriers | walks | prefix sums.
+struct Layout {
+    int q, ring, ring_stage, wide, scales, bars, walks, prefix, bytes;
+};
+
+constexpr int BAR_COUNT = 2 * MAX_RING + 2 * WIDE_RING + 2 + 2 + 2 + 2 + 2 + 1;  // odd: tmem slot and abort flag follow
+
+template <int DP, int QT, int TYPE>
+__host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
+{
+    Layout l{};
+    const int tile = DP / 64 * HALF_BYTES;
+    l.q = 0;
+    l.ring = QT * tile;
+    l.ring_stage = TYPE ? 128 * dim : tile;
+    l.wide = l.ring + ring * l.ring_stage;
+    l.scales = l.wide + (TYPE ? WIDE_RING * tile : 0);
+    l.bars = l.scales + (TYPE ? 2 * 3 * BN * 4 : 0);
+    l.walks = l.bars + BAR_COUNT * 8 + 8;
+    l.prefix = l.walks + 4 * QT * static_cast<int>(sizeof(WarpWalk));
+    l.bytes = l.prefix + (B + 1) * 4;
+    return l;
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > kWaitTimeoutNs / 10)
+            return;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int DP, int QT, int TYPE>
+__global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a)
+{
+    constexpr int kThreads = Shape<QT, TYPE>::kThreads;
+    constexpr int kHalves = DP / 64;
+    constexpr int kTile = kHalves * HALF_BYTES;
+    constexpr bool kQuant = TYPE != 0;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Layout lay = layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar0 = sbase + lay.bars;
+    auto ring_full = [&](int s) { return bar0 + 8u * s; };
+    auto ring_empty = [&](int s) { return bar0 + 8u * (MAX_RING + s); };
+    auto wide_full = [&](int s) { return bar0 + 8u * (2 * MAX_RING + s); };
+    auto wide_empty = [&](int s) { return bar0 + 8u * (2 * MAX_RING + WIDE_RING + s); };
+    constexpr int kRest = 2 * MAX_RING + 2 * WIDE_RING;
+    auto s_full = [&](int x) { return bar0 + 8u * (kRest + x); };
+    auto p_full = [&](int x) { return bar0 + 8u * (kRest + 2 + x); };
+    auto pv_done = [&](int s) { return bar0 + 8u * (kRest + 4 + s); };
+    auto q_full = [&](int s) { return bar0 + 8u * (kRest + 6 + s); };
+    auto scale_full = [&](int s) { return bar0 + 8u * (kRest + 8 + s); };
+    const uint32_t drain_bar = bar0 + 8u * (kRest + 10);
+    // what the MMAs read: the TMA ring itself, or the widened one
+    const int op_size = kQuant ? WIDE_RING : a.ring;
+    const uint32_t op_base = sbase + (kQuant ? lay.wide : lay.ring);
+    auto op_full = [&](int s) { return kQuant ? wide_full(s) : ring_full(s); };
+    auto op_empty = [&](int s) { return kQuant ? wide_empty(s) : ring_empty(s); };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.bars + BAR_COUNT * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int heads = a.q.heads, dim = a.cache.dim, ps = a.cache.page_size;
-    const long long r = static_cast<long long>(blockIdx.x) * kWarps + warp;
-    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        griddep_launch_dependents();
+        for (int s = 0; s < a.ring; ++s) {
+            mbar_init(ring_full(s), 1);
+            mbar_init(ring_empty(s), kQuant ? 4 : 1);
+        }
+        for (int s = 0; s < WIDE_RING; ++s) {
+            mbar_init(wide_full(s), 4);
+            mbar_init(wide_empty(s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full(s), 1);
+            mbar_init(p_full(s), 4);
+            mbar_init(pv_done(s), 1);
+            mbar_init(q_full(s), 4);
+            mbar_init(scale_full(s), 4);
+        }
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
     griddep_wait();
-    if (r >= static_cast<long long>(a.tokens.N) * heads)
-        return;
-    const int n = static_cast<int>(r / heads), h = static_cast<int>(r % heads), kvh = h / a.group;
-    const int b = warp_sequence_of(a.tokens.token_start, a.tokens.B, n, lane);
-    const int kv_len = a.tokens.kv_len[b];
-    const int pos = kv_len - a.tokens.token_start[b + 1] + n;
-    const int held = static_cast<int>(min(static_cast<long long>(kv_len), static_cast<long long>(a.tokens.max_pages) * ps));
-    const int hi = a.causal ? min(held, pos + 1) : held;
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    for (int d = lane; d < dim; d += 32)
-        qs[warp][d] = bf16_lo(a.q.data[n * a.q.token_stride + h * a.q.head_stride + d]) * a.scale_log2;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const int j = j0 + lane;
-        long long row = -1;
-        float s = -INFINITY, vs = 0.f;
-        if (j < hi) {
-            const int page = a.tokens.page_table[static_cast<long long>(b) * a.tokens.max_pages + j / ps];
-            if (page >= 0 && page < a.cache.pages)
-                row = (static_cast<long long>(page) * a.cache.heads + kvh) * ps + j % ps;
-            s = 0.f;
-            if (row >= 0) {
-                for (int d = 0; d < dim; ++d)
-                    s = fmaf(qs[warp][d], code_at(a.cache, a.cache.k, row, d), s);
-                vs = 1.f;
-                if (a.cache.type != 0) {
-                    s *= a.cache.k_scale[row];
-                    vs = a.cache.v_scale[row];
+
+    // key tiles of each sequence (for one cache head), then their running sum
+    const int B = a.tokens.B;
+    if (B <= kThreads / 32) {
+        if (warp < B) {
+            const Sequence s = sequence_at(a, warp);
+            const int nq = items_of(a, s);
+            int t = 0;
+            for (int qt = lane; qt < nq; qt += 32)
+                t += item_at(a, s, qt).tiles;
+            for (int o = 16; o > 0; o >>= 1)
+                t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == 0)
+                prefix[warp + 1] = t;
+        }
+    } else {
+        for (int b = threadIdx.x; b < B; b += kThreads) {
+            const Sequence s = sequence_at(a, b);
+            const int nq = items_of(a, s);
+            int t = 0;
+            for (int qt = 0; qt < nq; ++qt)
+                t += item_at(a, s, qt).tiles;
+            prefix[b + 1] = t;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int sum = 0;
+        if (lane == 0)
+            prefix[0] = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, t, o);
+                t += lane >= o ? x : 0;
+            }
+            t += sum;
+            if (b0 + lane < B)
+                prefix[b0 + lane + 1] = t;
+            sum = __shfl_sync(0xffffffffu, t, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const long long units = static_cast<long long>(prefix[B]) * a.cache.heads;
+    const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), units));
+    const int cta = blockIdx.x;
+    const bool works = cta < grid;
+
+    if (!works) {
+        if (threadIdx.x == 0)
+            a.records[cta].valid = 0;
+    } else if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        if constexpr (Shape<QT, TYPE>::kSplitRegs)
+            reg_dec<Shape<QT, TYPE>::kControlRegs>();
+        Walk w;
+        w.begin(a, prefix, units, grid, cta);
+        Segment g;
+        const int boxes = BN / a.box;
+        const int ps = a.cache.page_size, dim = a.cache.dim;
+        const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
+        int slot = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        while (ok && w.next(a, g)) {
+            const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
+            auto page_of = [&](int tile) {
+                const int tok = tile * BN + lane * a.box;
+                const bool need = lane < boxes && tok < g.item.hi && tok + a.box > g.item.lo;
+                return need ? min(max(__ldg(pt + tok / ps), 0), a.cache.pages - 1) : -1;
+            };
+            int page = page_of(g.tile);
+            for (int j = 0; j < g.tiles && ok; ++j) {
+                const int tok = (g.tile + j) * BN + lane * a.box;
+                const int next_page = j + 1 < g.tiles ? page_of(g.tile + j + 1) : -1;
+                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(ring_empty(slot), phase ^ 1u, abort_flag));
+                    if (!ok)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(ring_full(slot), bytes);
+                    __syncwarp();
+                    if (page >= 0) {
+                        const CUtensorMap *map = kv ? &map_v : &map_k;
+                        const uint32_t dst = sbase + lay.ring + slot * lay.ring_stage;
+                        if constexpr (kQuant) {
+                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot), 0, tok % ps, g.kvh, page);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_load_4d(dst + h * HALF_BYTES + lane * a.box * 128, map, ring_full(slot), h * 64,
+                                            tok % ps, g.kvh, page);
+                        }
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++slot == a.ring) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+                page = next_page;
+            }
+        }
+        if (!ok) {  // let the copies already issued land before the CTA leaves
+            for (long long n = issued > a.ring ? issued - a.ring : 0; n < issued; ++n)
+                drain_wait(ring_full(static_cast<int>(n % a.ring)), static_cast<uint32_t>((n / a.ring) & 1));
+        }
+    } else if (warp < 4) {
+        if constexpr (Shape<QT, TYPE>::kSplitRegs)
+            reg_dec<Shape<QT, TYPE>::kControlRegs>();
+        if (warp == 1 && lane == 0) {
+            // ------------------------------------------------------------ MMA issuer
+            const uint32_t fmt = kQuant ? 0u : (1u << 7 | 1u << 10);  // f16 or bf16 operands
+            const uint32_t shape = (1u << 4) | static_cast<uint32_t>(BM >> 4) << 24;
+            const uint32_t idesc_qk = fmt | shape | static_cast<uint32_t>(BN >> 3) << 17;
+            const uint32_t idesc_pv = fmt | shape | static_cast<uint32_t>(DP >> 3) << 17 | 1u << 16;  // V is MN-major
+            Walk w;
+            w.begin(a, prefix, units, grid, cta);
+            Segment g;
+            RingAt kr{0, 0}, vr{1, 0};
+            int cnt[2] = {0, 0};  // tiles done, per row tile (QT = 2) or in all (QT = 1, cnt[0])
+            uint32_t q_phase[2] = {0, 0};
+            bool ok = true;
+            auto qk = [&](int s, int sbuf, int slot) {
+                const uint32_t q = sbase + lay.q + s * kTile, k = op_base + slot * kTile;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const uint32_t o = (kk / 4) * HALF_BYTES + (kk % 4) * 32;
+                    umma_bf16(tmem + sbuf * BN, sw128_kmajor_desc(q + o), sw128_kmajor_desc(k + o), idesc_qk, kk > 0);
+                }
+                umma_commit(s_full(sbuf));
+            };
+            auto pv = [&](int s, int sbuf, int slot, bool first) {
+                const uint32_t v = op_base + slot * kTile;
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    umma_f16_tmem_a(tmem + 256 + s * 128, tmem + sbuf * BN + kk * 8,
+                                    sw128_mnmajor_desc(v + kk * 2048, HALF_BYTES), idesc_pv, !first || kk > 0);
+                umma_commit(pv_done(s));
+            };
+#define DF2_WAIT(bar, parity)                      \
+    if (!mbar_wait(bar, parity, abort_flag)) {     \
+        ok = false;                                \
+        break;                                     \
+    }
+            while (ok && w.next(a, g)) {
+                if constexpr (QT == 2) {
+                    const int mt = g.item.ntok > a.tpm ? 2 : 1;
+                    for (int s = 0; s < mt; ++s) {
+                        DF2_WAIT(q_full(s), q_phase[s]);
+                        q_phase[s] ^= 1u;
+                    }
+                    if (!ok)
+                        break;
+                    DF2_WAIT(op_full(kr.slot), kr.phase);
+                    tc_fence_after();
+                    for (int s = 0; s < mt; ++s)
+                        qk(s, s, kr.slot);
+                    umma_commit(op_empty(kr.slot));
+                    kr.step(op_size);
+                    for (int j = 0; j < g.tiles && ok; ++j) {
+                        const bool more = j + 1 < g.tiles;
+                        DF2_WAIT(op_full(vr.slot), vr.phase);
+                        for (int s = 0; s < mt; ++s) {
+                            DF2_WAIT(p_full(s), cnt[s] & 1);
+                            ++cnt[s];
+                            tc_fence_after();
+                            pv(s, s, vr.slot, j == 0);
+                            if (s == mt - 1)
+                                umma_commit(op_empty(vr.slot));
+                            if (more) {
+                                if (s == 0) {
+                                    DF2_WAIT(op_full(kr.slot), kr.phase);
+                                    tc_fence_after();
+                                }
+                                qk(s, s, kr.slot);
+                            }
+                        }
+                        vr.step(op_size);
+                        if (more) {
+                            umma_commit(op_empty(kr.slot));
+                            kr.step(op_size);
+                        }
+                    }
+                } else {
+                    DF2_WAIT(q_full(0), q_phase[0]);
+                    q_phase[0] ^= 1u;
+                    DF2_WAIT(op_full(kr.slot), kr.phase);
+                    tc_fence_after();
+                    qk(0, cnt[0] & 1, kr.slot);
+                    umma_commit(op_empty(kr.slot));
+                    kr.step(op_size);
+                    for (int j = 0; j < g.tiles; ++j) {
+                        const int sbuf = cnt[0] & 1;
+                        if (j + 1 < g.tiles) {
+                            DF2_WAIT(op_full(kr.slot), kr.phase);
+                            tc_fence_after();
+                            qk(0, sbuf ^ 1, kr.slot);
+                            umma_commit(op_empty(kr.slot));
+                            kr.step(op_size);
+                        }
+                        DF2_WAIT(op_full(vr.slot), vr.phase);
+                        DF2_WAIT(p_full(sbuf), (cnt[0] >> 1) & 1);
+                        ++cnt[0];
+                        tc_fence_after();
+                        pv(0, sbuf, vr.slot, j == 0);
+                        umma_commit(op_empty(vr.slot));
+                        vr.step(op_size);
+                    }
+                }
+            }
+#undef DF2_WAIT
+            // every MMA issued must finish before TMEM is released (in a healthy run all have)
+            umma_commit(drain_bar);
+            drain_wait(drain_bar, 0);
+        }
+    } else if (warp < 4 + 4 * QT) {
+        // -------------------------------------------------------------------- softmax, a thread per row
+        if constexpr (Shape<QT, TYPE>::kSplitRegs)
+            reg_inc<Shape<QT, TYPE>::kSoftRegs>();
+        const int s = QT == 2 ? (warp - 4) >> 2 : 0;
+        const int row = threadIdx.x - 128 - 128 * s;  // of the tile
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const int rt = row / a.group;  // token of the row within its tile
+        const int gi = row - rt * a.group;
+        const bool in_tile = row < a.tpm * a.group;
+        const int dim = a.cache.dim;
+        WarpWalk &ww = reinterpret_cast<WarpWalk *>(smem + lay.walks)[warp - 4];
+        if (lane == 0) {
+            ww.walk.begin(a, prefix, units, grid, cta);
+            ww.have[0] = ww.walk.next(a, ww.seg[0]);
+        }
+        __syncwarp();
+        RingAt vr{1, 0};
+        int cnt = 0;   // tiles this warpgroup has done
+        int tcnt = 0;  // tiles of the CTA
+        bool ok = true;
+        float qscale = 1.f, next_qscale = 1.f;  // 8-bit: row's scale * log2(e) * 2^-shift
+        if (s == 0 && row == 0)
+            a.records[cta].valid = 0;
+
+        // Q row of a segment's item into shared memory (swizzled, K-major)
+        auto active = [&](const Segment &x) { return s * a.tpm < x.item.ntok; };
+        auto row_live = [&](const Segment &x) { return in_tile && s * a.tpm + rt < x.item.ntok; };
+        auto load_q = [&](const Segment &x) {
+            if (row_live(x)) {
+                const uint16_t *src = a.q.data +
+                                      static_cast<long long>(x.start + x.item.tok0 + s * a.tpm + rt) * a.q.token_stride +
+                                      static_cast<long long>(x.kvh * a.group + gi) * a.q.head_stride;
+                uint8_t *dst = smem + lay.q + s * kTile + row * 128;
+                uint4 v[DP / 8];
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (8 * i < dim)
+                        v[i] = *reinterpret_cast<const uint4 *>(src + 8 * i);
+                    v[i].x = (v[i].x & a.q_and) ^ a.q_xor, v[i].y = (v[i].y & a.q_and) ^ a.q_xor;
+                    v[i].z = (v[i].z & a.q_and) ^ a.q_xor, v[i].w = (v[i].w & a.q_and) ^ a.q_xor;
+                    if constexpr (kQuant) {
+                        const uint32_t m = 0x7F807F80u;  // exponents
+                        top = __vmaxu2(__vmaxu2(top, v[i].x & m), __vmaxu2(v[i].y & m, __vmaxu2(v[i].z & m, v[i].w & m)));
+                    }
+                }
+                if constexpr (kQuant) {
+                    const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // biased
+                    const int shift = e == 0 ? 0 : min(14 - (e - 127), 126);
+                    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+                    next_qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i) {
+                        v[i].x = f16_pack(bf16_lo(v[i].x) * up, bf16_hi(v[i].x) * up);
+                        v[i].y = f16_pack(bf16_lo(v[i].y) * up, bf16_hi(v[i].y) * up);
+                        v[i].z = f16_pack(bf16_lo(v[i].z) * up, bf16_hi(v[i].z) * up);
+                        v[i].w = f16_pack(bf16_lo(v[i].w) * up, bf16_hi(v[i].w) * up);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i)
+                    *reinterpret_cast<uint4 *>(dst + (i / 8) * HALF_BYTES + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_full(s));
+        };
+
+        if (active(ww.seg[0]))
+            load_q(ww.seg[0]);
+        for (int which = 0; ok && ww.have[which]; which ^= 1) {
+            const Segment &g = ww.seg[which];
+            qscale = next_qscale;
+            const bool act = active(g);
+            const bool live = row_live(g);
+            const bool warp_live = __any_sync(0xffffffffu, live);
+            // keys the row sees, relative to the segment's tiles
+            int hi = 0x7FFFFFFF, lo = 0;  // rows of no token: whatever comes out goes nowhere
+            if (live) {
+                const int pos = g.item.p0 + s * a.tpm + rt;
+                hi = a.causal ? min(g.item.hi, pos + 1) : g.item.hi;
+                lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            }
+            float m = -INFINITY, l = 0.f;
+            const float sl2 = kQuant ? 1.f : a.scale_log2;
+            if (act) {
+                for (int j = 0; j < g.tiles; ++j) {
+                    const int t0 = (g.tile + j) * BN;
+                    const int sbuf = QT == 2 ? s : cnt & 1;
+                    const uint32_t s_phase = QT == 2 ? cnt & 1 : (cnt >> 1) & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(s_full(sbuf), s_phase, abort_flag));
+                    if (!ok)
+                        break;
+                    if constexpr (kQuant) {
+                        // S is there, so the tile's scales are, and no later tile's yet: the wait
+                        // only orders the reads after the writes
+                        ok = __all_sync(0xffffffffu, mbar_wait(scale_full(tcnt & 1), (tcnt >> 1) & 1, abort_flag));
+                        if (!ok)
+                            break;
+                    }
+                    tc_fence_after();
+                    const uint32_t s_addr = lane_base + sbuf * BN;
+                    const float *scales = reinterpret_cast<const float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
+                    if (warp_live) {
+                        uint32_t v[4][32];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tmem_ld_32x32b_x32(s_addr + 32 * i, v[i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tmem_wait_ld(v[i]);
+                        if constexpr (kQuant) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    v[i][c] = __float_as_uint(fmaf(__uint_as_float(v[i][c]) * scales[32 * i + c], qscale,
+                                                                   scales[BN + 32 * i + c]));
+                        }
+                        const int rlo = lo - t0, rhi = hi - t0;
+                        if (__any_sync(0xffffffffu, rlo > 0 || rhi < BN)) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (32 * i + c < rlo || 32 * i + c >= rhi)
+                                        v[i][c] = 0xFF800000u;
+                        }
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                top[i] = fmaxf(top[i], __uint_as_float(v[i][c]));
+                        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
+                        const bool move = live && rise > LAZY;
+                        if (j > 0 && __any_sync(0xffffffffu, move)) {
+                            // the products so far must be in before they are scaled
+                            ok = __all_sync(0xffffffffu, mbar_wait(pv_done(s), (cnt - 1) & 1, abort_flag));
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const float keep = move ? ex2(-rise) : 1.f;
+                            l = kQuant && move ? l * ex2(-0.5f * rise) * ex2(-0.5f * rise) : l * keep;
+#pragma unroll
+                            for (int c = 0; c < DP; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(lane_base + 256 + s * 128 + c, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                                tmem_st_32x32b_x16(lane_base + 256 + s * 128 + c, o);
+                            }
+                        }
+                        if (move)
+                            m = tile_top;
+                        const float base = m == -INFINITY ? 0.f : -m * sl2;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float p0 = ex2(fmaf(__uint_as_float(v[i][c]), sl2, base));
+                                const float p1 = ex2(fmaf(__uint_as_float(v[i][c + 1]), sl2, base));
+                                if constexpr (kQuant) {
+                                    sum[c & 2] = fmaf(p0, scales[2 * BN + 32 * i + c], sum[c & 2]);
+                                    sum[(c & 2) + 1] = fmaf(p1, scales[2 * BN + 32 * i + c + 1], sum[(c & 2) + 1]);
+                                    p[c / 2] = f16_pack(p0, p1);
+                                } else {
+                                    sum[c & 2] += p0;
+                                    sum[(c & 2) + 1] += p1;
+                                    p[c / 2] = bf16_pack(p0, p1);
+                                }
+                            }
+                            tmem_st_32x32b_x16(s_addr + 16 * i, p);
+                        }
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_wait_st();
+                    }
+                    if constexpr (!kQuant) {
+                        // rows of V that no row of the item sees may hold anything: 0 * NaN must not happen
+                        if (s == 0 && (t0 < g.item.lo || t0 + BN > g.item.hi)) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(ring_full(vr.slot), vr.phase, abort_flag));
+                            if (!ok)
+                                break;
+                            if (t0 + row < g.item.lo || t0 + row >= g.item.hi) {
+                                uint8_t *vrow = smem + lay.ring + vr.slot * lay.ring_stage + row * 128;
+#pragma unroll
+                                for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        *reinterpret_cast<uint4 *>(vrow + h * HALF_BYTES + 16 * i) =
+                                            make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async();
+                        }
+                        vr.step(a.ring);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full(sbuf));
+                    ++cnt;
+                    ++tcnt;
+                }
+            } else {
+                tcnt += g.tiles;
+            }
+            if (!ok)
+                break;
+            // the next item's queries go in while the last product of this one runs
+            if (lane == 0)
+                ww.have[which ^ 1] = ww.walk.next(a, ww.seg[which ^ 1]);
+            __syncwarp();
+            if (ww.have[which ^ 1] && active(ww.seg[which ^ 1]))
+                load_q(ww.seg[which ^ 1]);
+            if (act) {
+                ok = __all_sync(0xffffffffu, mbar_wait(pv_done(s), (cnt - 1) & 1, abort_flag));
+                if (!ok)
+                    break;
+                tc_fence_after();
+                const int tok = g.start + g.item.tok0 + s * a.tpm + rt;
+                const int head = g.kvh * a.group + gi;
+                const bool whole = g.first && g.last;
+                const int slot = 2 * cta + (g.u != cta * units / grid ? 1 : 0);
+                if (whole) {
+                    const float inv = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;
+                    uint16_t *dst = a.out.data + static_cast<long long>(tok) * a.out.token_stride +
+                                    static_cast<long long>(head) * a.out.head_stride;
+                    if (warp_live) {
+#pragma unroll
+                        for (int c = 0; c < DP; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
+                            tmem_wait_ld(o);
+                            if (live) {
+#pragma unroll
+                                for (int k = 0; k < 32; k += 8)
+                                    if (c + k < dim)
+                                        *reinterpret_cast<uint4 *>(dst + c + k) = make_uint4(
+                                            bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+                                            bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+                                            bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+                                            bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+                            }
+                        }
+                    }
+                    if (live && a.lse)
+                        a.lse[static_cast<long long>(tok) * a.q.heads + head] =
+                            (m * sl2 + log2f(l)) * 0.69314718055994530942f;
+                } else if (warp_live) {
+                    const long long at = static_cast<long long>(slot) * (QT * BM) + s * BM + row;
+                    float *dst = a.part_o + at * dim;
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
+                        tmem_wait_ld(o);
+                        if (live) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4)
+                                if (c + k < dim)
+                                    *reinterpret_cast<uint4 *>(dst + c + k) =
+                                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        }
+                    }
+                    if (live)
+                        a.part_ml[at] = make_float2(m * sl2, l);
+                }
+                if (s == 0 && row == 0 && g.first && !g.last) {
+                    const long long end = g.u + g.item.tiles - 1;  // the item's last unit
+                    SplitRecord rec;
+                    rec.valid = 1;
+                    rec.pad = 0;
+                    rec.first_slot = slot;
+                    rec.c0 = cta;
+                    rec.c1 = static_cast<int>(((end + 1) * grid - 1) / units);
+                    rec.kvh = g.kvh;
+                    rec.tok0 = g.start + g.item.tok0;
+                    rec.ntok = g.item.ntok;
+                    a.records[cta] = rec;
+                }
+                tc_fence_before();
+            }
+            __syncwarp();  // the other lanes are done with this segment before lane 0 writes over it
+        }
+    } else {
+        // -------------------------------------------------------------------- 8-bit codes to f16
+        if constexpr (kQuant) {
+            reg_dec<Shape<QT, TYPE>::kWideRegs>();
+            const int t = threadIdx.x - 128 * (1 + QT);
+            const int ps = a.cache.page_size, dim = a.cache.dim;
+            constexpr int kChunks = DP / 16;
+            Walk w;
+            w.begin(a, prefix, units, grid, cta);
+            Segment g;
+            int slot = 0, wslot = 0, tcnt = 0;
+            uint32_t phase = 0, wphase = 0;
+            bool ok = true;
+            while (ok && w.next(a, g)) {
+                const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
+                // this thread's key of a tile: its two scales
+                auto scales_of = [&](int tile) {
+                    const int tok = tile * BN + t;
+                    float2 r = make_float2(0.f, -1.f);  // no key there
+                    if (tok >= g.item.lo && tok < g.item.hi) {
+                        const int page = min(max(__ldg(pt + tok / ps), 0), a.cache.pages - 1);
+                        const long long at = (static_cast<long long>(page) * a.cache.heads + g.kvh) * ps + tok % ps;
+                        r = make_float2(a.cache.k_scale[at], a.cache.v_scale[at]);
+                    }
+                    return r;
+                };
+                float2 sc = scales_of(g.tile);
+                float top_lv = -INFINITY;  // this thread's largest log2 of a value scale in the segment
+                for (int j = 0; j < g.tiles && ok; ++j) {
+                    const int t0 = (g.tile + j) * BN;
+                    const float2 next_sc = j + 1 < g.tiles ? scales_of(g.tile + j + 1) : sc;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        ok = __all_sync(0xffffffffu, mbar_wait(wide_empty(wslot), wphase ^ 1u, abort_flag));
+                        if (!ok)
+                            break;
+                        if (kv == 0) {
+                            // the slot's last reader, the softmax two tiles back, is done: this wide
+                            // slot held that tile's V or a later operand
+                            float *sm = reinterpret_cast<float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
+                            float lv = sc.y > 0.f ? log2f(sc.y) : sc.y == 0.f ? -INFINITY : sc.y;
+                            float rv = sc.y != 0.f ? __fdiv_rn(1.f, sc.y) : 0.f;
+                            if (sc.y > 0.f)
+                                top_lv = fmaxf(top_lv, lv);
+                            if (__any_sync(0xffffffffu, sc.y == 0.f)) {
+                                // A row of zeros adds to l alone; any scale serves its codes.  One 2^60
+                                // below the largest seen keeps it from setting m' (P' of the others would
+                                // fall out of f16) and its own P' far above float32's least.
+                                float ref = top_lv;
+                                for (int o = 16; o > 0; o >>= 1)
+                                    ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+                                if (sc.y == 0.f) {
+                                    lv = fmaxf(floorf(ref) - 60.f, kLeastScale);
+                                    rv = exp2f(-lv);
+                                }
+                            }
+                            sm[t] = sc.x;
+                            sm[BN + t] = lv;
+                            sm[2 * BN + t] = rv;
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(scale_full(tcnt & 1));
+                        }
+                        ok = __all_sync(0xffffffffu, mbar_wait(ring_full(slot), phase, abort_flag));
+                        if (!ok)
+                            break;
+                        const uint8_t *src = smem + lay.ring + slot * lay.ring_stage;
+                        uint8_t *dst = smem + lay.wide + wslot * kTile;
+#pragma unroll
+                        for (int i = 0; i < kChunks; ++i) {
+                            const int at = i * 128 + t, r = at / kChunks, c = at % kChunks;
+                            const bool in = c * 16 < dim && t0 + r >= g.item.lo && t0 + r < g.item.hi;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            uint4 lo4 = v, hi4 = v;
+                            if (in) {
+                                v = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
+                                const uint2 w0 = widen4<TYPE>(v.x), w1 = widen4<TYPE>(v.y), w2 = widen4<TYPE>(v.z),
+                                            w3 = widen4<TYPE>(v.w);
+                                lo4 = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                                hi4 = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                            }
+                            // lanes of the two halves write opposite chunks of a pair, so eight lanes
+                            // cover all banks
+                            const int odd = c >> 2;
+                            uint8_t *d = dst + (c >> 2) * HALF_BYTES + r * 128;
+                            const int c0 = 2 * (c & 3);
+                            *reinterpret_cast<uint4 *>(d + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? hi4 : lo4;
+                            *reinterpret_cast<uint4 *>(d + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo4 : hi4;
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(ring_empty(slot));
+                            mbar_arrive(wide_full(wslot));
+                        }
+                        if (++slot == a.ring) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                        if (++wslot == WIDE_RING) {
+                            wslot = 0;
+                            wphase ^= 1u;
+                        }
+                    }
+                    sc = next_sc;
+                    ++tcnt;
                 }
             }
         }
-        float top = s;
-        for (int x = 16; x > 0; x >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float m2 = fmaxf(m, top);
-        const float keep = m2 == -INFINITY ? 0.f : exp2f(m - m2);
-        const float p = m2 == -INFINITY ? 0.f : exp2f(s - m2);
-        float sum = p;
-        for (int x = 16; x > 0; x >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l = l * keep + sum;
-        m = m2;
-        for (int i = 0; i < 4; ++i)
-            o[i] *= keep;
-        for (int k = 0; k < 32 && j0 + k < hi; ++k) {
-            const long long rk = __shfl_sync(0xffffffffu, row, k);
-            const float pk = __shfl_sync(0xffffffffu, p * vs, k);
-            if (rk >= 0)
-                for (int i = 0; i < 4; ++i)
-                    if (lane + 32 * i < dim)
-                        o[i] = fmaf(pk, code_at(a.cache, a.cache.v, rk, lane + 32 * i), o[i]);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *abort_flag)
+        atomicOr(a.status, kStatusTimeoutAttention);
+}
+
+struct CombineArgs {
+    HeadRows out;
+    float *lse;
+    int q_heads, group, tpm, dim, rows;
+    const SplitRecord *records;
+    const float2 *part_ml;
+    const float *part_o;
+};
+
+// Joins the pieces of the items that several CTAs worked on: a warp a row, in CTA order.
+__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const SplitRecord rec = a.records[blockIdx.x];
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int tile = row / BM, r = row % BM, rt = r / a.group, gi = r - rt * a.group;
+    const int t = tile * a.tpm + rt;
+    if (!rec.valid || rt >= a.tpm || t >= rec.ntok)
+        return;
+    const int n = rec.c1 - rec.c0 + 1;
+    auto at = [&](int i) {
+        const int slot = i == 0 ? rec.first_slot : 2 * (rec.c0 + i);
+        return static_cast<long long>(slot) * a.rows + row;
+    };
+    float top = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        top = fmaxf(top, a.part_ml[at(i)].x);
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float wgt = 0.f;
+        if (i0 + lane < n) {
+            const float2 ml = a.part_ml[at(i0 + lane)];
+            wgt = exp2f(ml.x - base);
+            // in one power: with an 8-bit cache the maximum carries a value's scale, and the weight
+            // alone may fall below what float32 holds
+            l += ml.y > 0.f ? exp2f(ml.x - base + log2f(ml.y)) : ml.y == 0.f ? 0.f : ml.y;
+        }
+        const int m = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < m; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, wgt, i);
+            if (4 * lane < a.dim) {
+                const float4 o = *reinterpret_cast<const float4 *>(a.part_o + at(i0 + i) * a.dim + 4 * lane);
+                acc.x = fmaf(wi, o.x, acc.x), acc.y = fmaf(wi, o.y, acc.y);
+                acc.z = fmaf(wi, o.z, acc.z), acc.w = fmaf(wi, o.w, acc.w);
+            }
         }
     }
+    for (int o = 16; o > 0; o >>= 1)
+        l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < dim)
-            a.out.data[n * a.out.token_stride + h * a.out.head_stride + lane + 32 * i] =
-                static_cast<uint16_t>(bf16_pack(o[i] * inv, 0.f));
+    const long long tok = rec.tok0 + t;
+    const int head = rec.kvh * a.group + gi;
+    if (4 * lane < a.dim)
+        *reinterpret_cast<uint2 *>(a.out.data + tok * a.out.token_stride + head * a.out.head_stride + 4 * lane) =
+            make_uint2(bf16_pack(acc.x * inv, acc.y * inv), bf16_pack(acc.z * inv, acc.w * inv));
     if (a.lse && lane == 0)
-        a.lse[static_cast<long long>(n) * heads + h] = (m + log2f(l)) * 0.69314718055994530942f;
+        a.lse[tok * a.q_heads + head] = (top + log2f(l)) * 0.69314718055994530942f;
+}
+
+// Row tiles an item has: two when some sequence may have more rows than one holds.
+int row_tiles(const TokenBatch &t, int group) { return t.max_new > BM / group ? 2 : 1; }
+
+struct Scratch {
+    size_t records, ml, o, bytes;
+};
+
+Scratch scratch_of(int sms, int tiles, int dim)
+{
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Scratch s{};
+    const size_t rows = static_cast<size_t>(2) * sms * tiles * BM;
+    s.records = 0;
+    s.ml = up(static_cast<size_t>(sms) * sizeof(SplitRecord));
+    s.o = s.ml + up(rows * sizeof(float2));
+    s.bytes = s.o + up(rows * dim * sizeof(float));
+    return s;
+}
+
+// A cache tensor [pages, heads, page_size, dim]: boxes of `box` rows of one page, 64 bf16 elements
+// wide with the 128-byte swizzle, or whole rows of 8-bit codes as they lie.
+cudaError_t encode_cache(CUtensorMap *map, const PagedCache &c, const void *base, int box)
+{
+    auto encode = tensor_map_encoder();
+    if (!encode)
+        return cudaErrorNotSupported;
+    const bool wide = c.type == 0;
+    const cuuint64_t es = wide ? 2 : 1;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {dims[0] * es, dims[0] * dims[1] * es, dims[0] * dims[1] * dims[2] * es};
+    const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(wide ? 64 : c.dim), static_cast<cuuint32_t>(box), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                              const_cast<void *>(base), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int DP, int QT, int TYPE>
+cudaError_t launch(Args a, int sms, cudaStream_t stream)
+{
+    a.ring = MAX_RING;
+    while (a.ring > 3 && layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024 > SMEM_LIMIT)
+        --a.ring;
+    const int smem = layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024;
+    if (smem > SMEM_LIMIT)
+        return cudaErrorInvalidConfiguration;
+    CUtensorMap mk, mv;
+    cudaError_t e;
+    if ((e = encode_cache(&mk, a.cache, a.cache.k, a.box)) != cudaSuccess ||
+        (e = encode_cache(&mv, a.cache, a.cache.v, a.box)) != cudaSuccess)
+        return e;
+    auto kern = attention_kernel<DP, QT, TYPE>;
+    if ((e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) != cudaSuccess)
+        return e;
+    return launch_dependent(kern, dim3(static_cast<unsigned>(sms)), dim3(Shape<QT, TYPE>::kThreads),
+                            static_cast<size_t>(smem), stream, mk, mv, a);
+}
+
+template <int DP, int QT>
+cudaError_t launch_type(const Args &a, int sms, cudaStream_t stream)
+{
+    switch (a.cache.type) {
+    case 0: return launch<DP, QT, 0>(a, sms, stream);
+    case 1: return launch<DP, QT, 1>(a, sms, stream);
+    default: return launch<DP, QT, 2>(a, sms, stream);
+    }
 }
 
 }  // namespace
 
-size_t paged_attention_scratch(const PagedCache &, const TokenBatch &, int) { return 0; }
+size_t paged_attention_scratch(const PagedCache &cache, const TokenBatch &tokens, int q_heads)
+{
+    return scratch_of(device_sm_count(), row_tiles(tokens, q_heads / cache.heads), cache.dim).bytes;
+}
 
 cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &tokens, const AttentionOptions &opt,
-                                   const HeadRows &q, const HeadRows &out, float *lse, uint32_t *, void *,
-                                   cudaStream_t stream)
+                                   const HeadRows &q, const HeadRows &out, float *lse, uint32_t *status,
+                                   void *scratch, cudaStream_t stream)
 {
-    AttnArgs a{};
+    const int sms = device_sm_count();
+    Args a{};
     a.cache = cache;
     a.tokens = tokens;
     a.q = q;
     a.out = out;
     a.lse = lse;
-    a.scale_log2 = opt.scale * 1.44269504088896340736f;
+    const float scale = opt.scale == 0.f ? 1.f : std::fabs(opt.scale);
+    a.scale_log2 = scale * 1.44269504088896340736f;
+    a.q_and = opt.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    a.q_xor = opt.scale < 0.f ? 0x80008000u : 0u;
     a.causal = opt.causal;
-    a.window = opt.window;
+    a.window = opt.window >= tokens.max_pages * cache.page_size ? 0 : opt.window;
     a.group = q.heads / cache.heads;
-    const long long rows = static_cast<long long>(tokens.N) * q.heads;
-    return launch_dependent(attention_kernel, dim3(static_cast<unsigned>((rows + kWarps - 1) / kWarps)),
-                            dim3(kWarps * 32), 0, stream, a);
+    const int tiles = row_tiles(tokens, a.group);
+    a.tpm = BM / a.group;
+    a.span = tiles * a.tpm;
+    a.box = std::gcd(cache.page_size, BN);
+    a.status = status;
+    const Scratch s = scratch_of(sms, tiles, cache.dim);
+    uint8_t *p = static_cast<uint8_t *>(scratch);
+    a.records = reinterpret_cast<SplitRecord *>(p + s.records);
+    a.part_ml = reinterpret_cast<float2 *>(p + s.ml);
+    a.part_o = reinterpret_cast<float *>(p + s.o);
+    cudaError_t e;
+    if (cache.dim <= 64)
+        e = tiles == 1 ? launch_type<64, 1>(a, sms, stream) : launch_type<64, 2>(a, sms, stream);
+    else
+        e = tiles == 1 ? launch_type<128, 1>(a, sms, stream) : launch_type<128, 2>(a, sms, stream);
+    if (e != cudaSuccess)
+        return e;
+    CombineArgs c{};
+    c.out = out;
+    c.lse = lse;
+    c.q_heads = q.heads;
+    c.group = a.group;
+    c.tpm = a.tpm;
+    c.dim = cache.dim;
+    c.rows = tiles * BM;
+    c.records = a.records;
+    c.part_ml = a.part_ml;
+    c.part_o = a.part_o;
+    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), static_cast<unsigned>(c.rows / 8)),
+                            dim3(256), 0, stream, c);
 }
 
 }  // namespace df2

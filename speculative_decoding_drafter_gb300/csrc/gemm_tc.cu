@@ -57,6 +57,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 #include "topk.cuh"
 
 namespace df2 {
@@ -596,25 +597,6 @@ __global__ void __launch_bounds__(64 + MT * BM, 1)
                 args.group_done[group] = 0u;
         }
     }
-}
-
-// The driver's encoder, looked up on first use (again after a failed lookup); safe to call from
-// several host threads.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
-{
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> cached{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 fn = cached.load(std::memory_order_acquire);
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess) {
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-            cached.store(fn, std::memory_order_release);
-        }
-    }
-    return fn;
 }
 
 // CTAs of a pair kernel resident at once on the current device (clusters of two need two SMs

@@ -8,7 +8,7 @@
 namespace df2 {
 
 // The sequence that packed token n belongs to: the largest b with token_start[b] <= n.  One
-// warp, 32 probes a step (B <= 4096: three loads deep at most).
+// warp, 32 probes a step (B <= 2048: three loads deep at most).
 __device__ __forceinline__ int warp_sequence_of(const int32_t *token_start, int B, int n, int lane)
 {
     int lo = 0, hi = B;
