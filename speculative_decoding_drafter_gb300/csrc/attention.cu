@@ -13,9 +13,14 @@
 //
 // Roles of a CTA: warp 0 loads K and V tiles by TMA, a box per run of a page; one thread of warp 1
 // issues the MMAs; a warpgroup per row tile does the softmax, a thread per row, S read from and P
-// written back to tensor memory; with an 8-bit cache one more warpgroup widens the codes to f16.
+// written back to tensor memory; with an 8-bit cache two more warpgroups
+// widen the codes to f16, one K's and one V's.
 //   S = Q K^T   both K-major from shared memory          D[128 x 128] in TMEM
 //   O += P V    P from TMEM over S, V as it lies (its rows are the K dimension: MN-major B)
+// Few rows (a draft block of one cache head is often 8 to 64 of them) leave most of a 128-row tile
+// empty, and a thread that walks 128 scores is then the longest step of a tile.  The tile holds
+// such rows FOLD = 2 or 4 times over instead: every copy takes 128 / FOLD of a tile's keys (its P
+// is zero elsewhere), with its own m and l, and the copies are added up at the end of the item.
 // 8-bit caches: codes are exact in f16, so K's scale multiplies the score, and V's goes into the
 // exponent: x'_j = x_j + log2(vs_j), P'_j = 2^(x'_j - m'), o = sum P'_j code_j, l = sum P'_j / vs_j,
 // which keeps P' in f16's range whatever the values' size.  Queries go to f16 by a power of two per
@@ -28,6 +33,7 @@
 #include <cstdint>
 #include <numeric>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -229,13 +235,16 @@ __device__ __forceinline__ uint2 widen4(uint32_t w)
 
 template <int QT, int TYPE>
 struct Shape {
-    static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 1 : 0));
+    static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 2 : 0));
     // registers of a thread after the roles part: control, softmax, widening (their sum times 128
     // is at most what the launch holds: 65536 / threads, a multiple of 8, times the threads)
-    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 184 : 216;
-    static constexpr int kWideRegs = QT == 2 ? 80 : 160;
-    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 64 : 128;
+    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 144 : 216;
+    static constexpr int kWideRegs = QT == 2 ? 64 : 104;
+    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 64 : 88;
     static constexpr bool kSplitRegs = kThreads > 256;
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static_assert(!kSplitRegs || kControlRegs + QT * kSoftRegs + (TYPE ? 2 * kWideRegs : 0) <=
+                                     kThreads / 128 * kLaunchRegs, "setmaxnreg.inc would wait forever");
 };
 
 // A softmax warp's walk, kept in shared memory: its registers hold a row of scores.
@@ -245,12 +254,12 @@ struct WarpWalk {
     int have[2];
 };
 
-// Shared memory: Q tiles | TMA ring | widened ring (8-bit) | scales (8-bit) | barriers | walks | prefix sums.
+// Shared memory: Q tiles | TMA ring | widened ring (8-bit) | scales (8-bit) | copies' (m, l) | barriers | walks | prefix sums.
 struct Layout {
-    int q, ring, ring_stage, wide, scales, bars, walks, prefix, bytes;
+    int q, ring, ring_stage, wide, scales, fold, bars, walks, prefix, bytes;
 };
 
-constexpr int BAR_COUNT = 2 * MAX_RING + 2 * WIDE_RING + 2 + 2 + 2 + 2 + 2 + 1;  // odd: tmem slot and abort flag follow
+constexpr int BAR_COUNT = 3 * MAX_RING + 3 * WIDE_RING + 2 + 2 + 2 + 2 + 2 + 1 + 1;  // tmem slot and abort flag follow
 
 template <int DP, int QT, int TYPE>
 __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
@@ -262,7 +271,8 @@ __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
     l.ring_stage = TYPE ? 128 * dim : tile;
     l.wide = l.ring + ring * l.ring_stage;
     l.scales = l.wide + (TYPE ? WIDE_RING * tile : 0);
-    l.bars = l.scales + (TYPE ? 2 * 3 * BN * 4 : 0);
+    l.fold = l.scales + (TYPE ? 2 * 3 * BN * 4 : 0);
+    l.bars = l.fold + (QT == 1 ? BM * 8 : 0);
     l.walks = l.bars + BAR_COUNT * 8 + 8;
     l.prefix = l.walks + 4 * QT * static_cast<int>(sizeof(WarpWalk));
     l.bytes = l.prefix + (B + 1) * 4;
@@ -277,6 +287,27 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
             return;
 }
 
+// N consecutive columns of this thread's lane, all in flight before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 32)
+        tmem_ld_32x32b_x32(taddr + i, reinterpret_cast<uint32_t(&)[32]>(v[i]));
+#pragma unroll
+    for (int i = 0; i < N; i += 32)
+        tmem_wait_ld(reinterpret_cast<uint32_t(&)[32]>(v[i]));
+}
+
+__device__ __forceinline__ uint64_t load2(const uint32_t *v) { return f2(__uint_as_float(v[0]), __uint_as_float(v[1])); }
+
+__device__ __forceinline__ void store2(uint32_t *v, uint64_t x)
+{
+    const float2 f = f2_split(x);
+    v[0] = __float_as_uint(f.x);
+    v[1] = __float_as_uint(f.y);
+}
+
 template <int N>
 __device__ __forceinline__ void reg_dec()
 {
@@ -288,7 +319,7 @@ __device__ __forceinline__ void reg_inc()
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int DP, int QT, int TYPE>
+template <int DP, int QT, int TYPE, int FOLD>
 __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a)
 {
@@ -296,27 +327,33 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     constexpr int kHalves = DP / 64;
     constexpr int kTile = kHalves * HALF_BYTES;
     constexpr bool kQuant = TYPE != 0;
+    constexpr int kRows = BM / FOLD;  // distinct rows of a tile
+    constexpr int kCols = BN / FOLD;  // keys of a tile that a thread takes
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Layout lay = layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + lay.bars;
-    auto ring_full = [&](int s) { return bar0 + 8u * s; };
-    auto ring_empty = [&](int s) { return bar0 + 8u * (MAX_RING + s); };
-    auto wide_full = [&](int s) { return bar0 + 8u * (2 * MAX_RING + s); };
-    auto wide_empty = [&](int s) { return bar0 + 8u * (2 * MAX_RING + WIDE_RING + s); };
-    constexpr int kRest = 2 * MAX_RING + 2 * WIDE_RING;
+    // A barrier's phases are told apart by parity, so whoever waits on one must wait for every phase
+    // of it.  The slots of the odd-sized widened ring (and of the TMA ring, if its size is odd) hold
+    // a K and a V in turn, which different warpgroups widen: each has barriers of its own.
+    auto ring_full = [&](int s, int kv) { return bar0 + 8u * (s + (kQuant ? kv * MAX_RING : 0)); };
+    auto ring_empty = [&](int s) { return bar0 + 8u * (2 * MAX_RING + s); };
+    auto wide_full = [&](int s) { return bar0 + 8u * (3 * MAX_RING + s); };
+    auto wide_empty = [&](int s, int next_kv) { return bar0 + 8u * (3 * MAX_RING + WIDE_RING * (1 + next_kv) + s); };
+    constexpr int kRest = 3 * MAX_RING + 3 * WIDE_RING;
     auto s_full = [&](int x) { return bar0 + 8u * (kRest + x); };
     auto p_full = [&](int x) { return bar0 + 8u * (kRest + 2 + x); };
     auto pv_done = [&](int s) { return bar0 + 8u * (kRest + 4 + s); };
     auto q_full = [&](int s) { return bar0 + 8u * (kRest + 6 + s); };
     auto scale_full = [&](int s) { return bar0 + 8u * (kRest + 8 + s); };
     const uint32_t drain_bar = bar0 + 8u * (kRest + 10);
+    const uint32_t fold_bar = bar0 + 8u * (kRest + 11);
     // what the MMAs read: the TMA ring itself, or the widened one
     const int op_size = kQuant ? WIDE_RING : a.ring;
     const uint32_t op_base = sbase + (kQuant ? lay.wide : lay.ring);
-    auto op_full = [&](int s) { return kQuant ? wide_full(s) : ring_full(s); };
-    auto op_empty = [&](int s) { return kQuant ? wide_empty(s) : ring_empty(s); };
+    auto op_full = [&](int s) { return kQuant ? wide_full(s) : ring_full(s, 0); };
+    auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, 1 - kv) : ring_empty(s); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.bars + BAR_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
@@ -325,12 +362,15 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     if (threadIdx.x == 0) {
         griddep_launch_dependents();
         for (int s = 0; s < a.ring; ++s) {
-            mbar_init(ring_full(s), 1);
+            mbar_init(ring_full(s, 0), 1);
+            if (kQuant)
+                mbar_init(ring_full(s, 1), 1);
             mbar_init(ring_empty(s), kQuant ? 4 : 1);
         }
         for (int s = 0; s < WIDE_RING; ++s) {
             mbar_init(wide_full(s), 4);
-            mbar_init(wide_empty(s), 1);
+            mbar_init(wide_empty(s, 0), 1);
+            mbar_init(wide_empty(s, 1), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full(s), 1);
@@ -340,6 +380,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_init(scale_full(s), 4);
         }
         mbar_init(drain_bar, 1);
+        mbar_init(fold_bar, 4);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&map_k);
@@ -436,17 +477,17 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     if (!ok)
                         break;
                     if (lane == 0)
-                        mbar_arrive_expect_tx(ring_full(slot), bytes);
+                        mbar_arrive_expect_tx(ring_full(slot, kv), bytes);
                     __syncwarp();
                     if (page >= 0) {
                         const CUtensorMap *map = kv ? &map_v : &map_k;
                         const uint32_t dst = sbase + lay.ring + slot * lay.ring_stage;
                         if constexpr (kQuant) {
-                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot), 0, tok % ps, g.kvh, page);
+                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot, kv), 0, tok % ps, g.kvh, page);
                         } else {
 #pragma unroll
                             for (int h = 0; h < kHalves; ++h)
-                                tma_load_4d(dst + h * HALF_BYTES + lane * a.box * 128, map, ring_full(slot), h * 64,
+                                tma_load_4d(dst + h * HALF_BYTES + lane * a.box * 128, map, ring_full(slot, kv), h * 64,
                                             tok % ps, g.kvh, page);
                         }
                     }
@@ -462,17 +503,23 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         }
         if (!ok) {  // let the copies already issued land before the CTA leaves
             for (long long n = issued > a.ring ? issued - a.ring : 0; n < issued; ++n)
-                drain_wait(ring_full(static_cast<int>(n % a.ring)), static_cast<uint32_t>((n / a.ring) & 1));
+                drain_wait(ring_full(static_cast<int>(n % a.ring), static_cast<int>(n & 1)),
+                           static_cast<uint32_t>((n / a.ring) >> (kQuant && (a.ring & 1) ? 1 : 0)) & 1u);
         }
     } else if (warp < 4) {
         if constexpr (Shape<QT, TYPE>::kSplitRegs)
             reg_dec<Shape<QT, TYPE>::kControlRegs>();
-        if (warp == 1 && lane == 0) {
+        if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
+            // The warp walks and waits together and one elected lane issues: operands are then
+            // warp-uniform for the compiler, which costs far less per MMA than a lone lane's.
             const uint32_t fmt = kQuant ? 0u : (1u << 7 | 1u << 10);  // f16 or bf16 operands
             const uint32_t shape = (1u << 4) | static_cast<uint32_t>(BM >> 4) << 24;
             const uint32_t idesc_qk = fmt | shape | static_cast<uint32_t>(BN >> 3) << 17;
             const uint32_t idesc_pv = fmt | shape | static_cast<uint32_t>(DP >> 3) << 17 | 1u << 16;  // V is MN-major
+            const uint64_t k_desc = sw128_kmajor_desc(0), v_desc = sw128_mnmajor_desc(0, HALF_BYTES);
+            const uint32_t k_lo = static_cast<uint32_t>(k_desc), k_hi = static_cast<uint32_t>(k_desc >> 32);
+            const uint32_t v_lo = static_cast<uint32_t>(v_desc), v_hi = static_cast<uint32_t>(v_desc >> 32);
             Walk w;
             w.begin(a, prefix, units, grid, cta);
             Segment g;
@@ -481,26 +528,41 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             uint32_t q_phase[2] = {0, 0};
             bool ok = true;
             auto qk = [&](int s, int sbuf, int slot) {
-                const uint32_t q = sbase + lay.q + s * kTile, k = op_base + slot * kTile;
+                const uint32_t q = k_lo + ((sbase + lay.q + s * kTile) >> 4);
+                const uint32_t k = k_lo + ((op_base + __shfl_sync(0xffffffffu, slot, 0) * kTile) >> 4);
+                const uint32_t d = tmem + __shfl_sync(0xffffffffu, sbuf, 0) * BN;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    const uint32_t o = (kk / 4) * HALF_BYTES + (kk % 4) * 32;
-                    umma_bf16(tmem + sbuf * BN, sw128_kmajor_desc(q + o), sw128_kmajor_desc(k + o), idesc_qk, kk > 0);
+                    for (int kk = 0; kk < DP / 16; ++kk) {
+                        const uint32_t o = ((kk / 4) * HALF_BYTES + (kk % 4) * 32) >> 4;
+                        umma_bf16(d, desc_at(q + o, k_hi), desc_at(k + o, k_hi), idesc_qk, kk > 0);
+                    }
+                    umma_commit(s_full(sbuf));
                 }
-                umma_commit(s_full(sbuf));
+                __syncwarp();
             };
             auto pv = [&](int s, int sbuf, int slot, bool first) {
-                const uint32_t v = op_base + slot * kTile;
+                const uint32_t v = v_lo + ((op_base + __shfl_sync(0xffffffffu, slot, 0) * kTile) >> 4);
+                const uint32_t p = tmem + __shfl_sync(0xffffffffu, sbuf, 0) * BN;
+                const uint32_t d = tmem + 256 + s * 128;
+                const uint32_t acc = __shfl_sync(0xffffffffu, first ? 0u : 1u, 0);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    umma_f16_tmem_a(tmem + 256 + s * 128, tmem + sbuf * BN + kk * 8,
-                                    sw128_mnmajor_desc(v + kk * 2048, HALF_BYTES), idesc_pv, !first || kk > 0);
-                umma_commit(pv_done(s));
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        umma_f16_tmem_a(d, p + kk * 8, desc_at(v + kk * (2048 >> 4), v_hi), idesc_pv, kk > 0 ? 1u : acc);
+                    umma_commit(pv_done(s));
+                }
+                __syncwarp();
             };
-#define DF2_WAIT(bar, parity)                      \
-    if (!mbar_wait(bar, parity, abort_flag)) {     \
-        ok = false;                                \
-        break;                                     \
+            auto commit = [&](uint32_t bar) {
+                if (elect_one())
+                    umma_commit(bar);
+                __syncwarp();
+            };
+#define DF2_WAIT(bar, parity)                                               \
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) { \
+        ok = false;                                                         \
+        break;                                                              \
     }
             while (ok && w.next(a, g)) {
                 if constexpr (QT == 2) {
@@ -515,7 +577,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     tc_fence_after();
                     for (int s = 0; s < mt; ++s)
                         qk(s, s, kr.slot);
-                    umma_commit(op_empty(kr.slot));
+                    commit(op_empty(kr.slot, 0));
                     kr.step(op_size);
                     for (int j = 0; j < g.tiles && ok; ++j) {
                         const bool more = j + 1 < g.tiles;
@@ -526,7 +588,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             tc_fence_after();
                             pv(s, s, vr.slot, j == 0);
                             if (s == mt - 1)
-                                umma_commit(op_empty(vr.slot));
+                                commit(op_empty(vr.slot, 1));
                             if (more) {
                                 if (s == 0) {
                                     DF2_WAIT(op_full(kr.slot), kr.phase);
@@ -537,7 +599,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         }
                         vr.step(op_size);
                         if (more) {
-                            umma_commit(op_empty(kr.slot));
+                            commit(op_empty(kr.slot, 0));
                             kr.step(op_size);
                         }
                     }
@@ -547,7 +609,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     DF2_WAIT(op_full(kr.slot), kr.phase);
                     tc_fence_after();
                     qk(0, cnt[0] & 1, kr.slot);
-                    umma_commit(op_empty(kr.slot));
+                    commit(op_empty(kr.slot, 0));
                     kr.step(op_size);
                     for (int j = 0; j < g.tiles; ++j) {
                         const int sbuf = cnt[0] & 1;
@@ -555,7 +617,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             DF2_WAIT(op_full(kr.slot), kr.phase);
                             tc_fence_after();
                             qk(0, sbuf ^ 1, kr.slot);
-                            umma_commit(op_empty(kr.slot));
+                            commit(op_empty(kr.slot, 0));
                             kr.step(op_size);
                         }
                         DF2_WAIT(op_full(vr.slot), vr.phase);
@@ -563,14 +625,14 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         ++cnt[0];
                         tc_fence_after();
                         pv(0, sbuf, vr.slot, j == 0);
-                        umma_commit(op_empty(vr.slot));
+                        commit(op_empty(vr.slot, 1));
                         vr.step(op_size);
                     }
                 }
             }
 #undef DF2_WAIT
             // every MMA issued must finish before TMEM is released (in a healthy run all have)
-            umma_commit(drain_bar);
+            commit(drain_bar);
             drain_wait(drain_bar, 0);
         }
     } else if (warp < 4 + 4 * QT) {
@@ -580,9 +642,11 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         const int s = QT == 2 ? (warp - 4) >> 2 : 0;
         const int row = threadIdx.x - 128 - 128 * s;  // of the tile
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const int rt = row / a.group;  // token of the row within its tile
-        const int gi = row - rt * a.group;
-        const bool in_tile = row < a.tpm * a.group;
+        const int trow = row % kRows;
+        const int col0 = row / kRows * kCols;  // this copy's keys
+        const int rt = trow / a.group;  // token of the row within its tile
+        const int gi = trow - rt * a.group;
+        const bool in_tile = trow < a.tpm * a.group;
         const int dim = a.cache.dim;
         WarpWalk &ww = reinterpret_cast<WarpWalk *>(smem + lay.walks)[warp - 4];
         if (lane == 0) {
@@ -644,6 +708,17 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 mbar_arrive(q_full(s));
         };
 
+        // all four warps of the (one) softmax warpgroup meet; false on a timeout
+        uint32_t fold_phase = 0;
+        auto fold_sync = [&]() {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(fold_bar);
+            const bool met = __all_sync(0xffffffffu, mbar_wait(fold_bar, fold_phase, abort_flag));
+            fold_phase ^= 1u;
+            return met;
+        };
+
         if (active(ww.seg[0]))
             load_q(ww.seg[0]);
         for (int which = 0; ok && ww.have[which]; which ^= 1) {
@@ -680,36 +755,31 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     const uint32_t s_addr = lane_base + sbuf * BN;
                     const float *scales = reinterpret_cast<const float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
                     if (warp_live) {
-                        uint32_t v[4][32];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tmem_ld_32x32b_x32(s_addr + 32 * i, v[i]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tmem_wait_ld(v[i]);
+                        uint32_t v[kCols];
+                        tmem_ld_row<kCols>(s_addr + col0, v);
                         if constexpr (kQuant) {
+                            const uint64_t qs2 = f2(qscale, qscale);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    v[i][c] = __float_as_uint(fmaf(__uint_as_float(v[i][c]) * scales[32 * i + c], qscale,
-                                                                   scales[BN + 32 * i + c]));
+                            for (int c = 0; c < kCols; c += 4) {
+                                const float4 ks = *reinterpret_cast<const float4 *>(scales + col0 + c);
+                                const float4 lv = *reinterpret_cast<const float4 *>(scales + BN + col0 + c);
+                                store2(v + c, fma2(mul2(load2(v + c), f2(ks.x, ks.y)), qs2, f2(lv.x, lv.y)));
+                                store2(v + c + 2, fma2(mul2(load2(v + c + 2), f2(ks.z, ks.w)), qs2, f2(lv.z, lv.w)));
+                            }
                         }
-                        const int rlo = lo - t0, rhi = hi - t0;
-                        if (__any_sync(0xffffffffu, rlo > 0 || rhi < BN)) {
+                        const int rlo = lo - t0 - col0, rhi = hi - t0 - col0;
+                        if (__any_sync(0xffffffffu, rlo > 0 || rhi < kCols)) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    if (32 * i + c < rlo || 32 * i + c >= rhi)
-                                        v[i][c] = 0xFF800000u;
+                            for (int c = 0; c < kCols; ++c)
+                                if (c < rlo || c >= rhi)
+                                    v[c] = 0xFF800000u;
                         }
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
+                        for (int c = 0; c < kCols; c += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                top[i] = fmaxf(top[i], __uint_as_float(v[i][c]));
+                                top[i] = fmaxf(top[i], fmaxf(__uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1])));
                         const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
                         const bool move = live && rise > LAZY;
@@ -735,33 +805,52 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         if (move)
                             m = tile_top;
                         const float base = m == -INFINITY ? 0.f : -m * sl2;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        const uint64_t base2 = f2(base, base), sl22 = f2(sl2, sl2);
+                        uint64_t sum2[2] = {0, 0};
+                        if constexpr (FOLD > 1) {  // the other copies' keys
+                            uint32_t z[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                            for (int k = 0; k < 16; ++k)
+                                z[k] = 0;
+#pragma unroll
+                            for (int c = 0; c < BN / 2; c += 16)
+                                if (2 * c < col0 || 2 * c >= col0 + kCols)
+                                    tmem_st_32x32b_x16(s_addr + c, z);
+                        }
+#pragma unroll
+                        for (int c0 = 0; c0 < kCols; c0 += 32) {
                             uint32_t p[16];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 2) {
-                                const float p0 = ex2(fmaf(__uint_as_float(v[i][c]), sl2, base));
-                                const float p1 = ex2(fmaf(__uint_as_float(v[i][c + 1]), sl2, base));
+                            for (int c = 0; c < 32; c += 4) {
+                                uint64_t x0 = load2(v + c0 + c), x1 = load2(v + c0 + c + 2);
                                 if constexpr (kQuant) {
-                                    sum[c & 2] = fmaf(p0, scales[2 * BN + 32 * i + c], sum[c & 2]);
-                                    sum[(c & 2) + 1] = fmaf(p1, scales[2 * BN + 32 * i + c + 1], sum[(c & 2) + 1]);
-                                    p[c / 2] = f16_pack(p0, p1);
+                                    x0 = add2(x0, base2), x1 = add2(x1, base2);
                                 } else {
-                                    sum[c & 2] += p0;
-                                    sum[(c & 2) + 1] += p1;
-                                    p[c / 2] = bf16_pack(p0, p1);
+                                    x0 = fma2(x0, sl22, base2), x1 = fma2(x1, sl22, base2);
+                                }
+                                const float2 y0 = f2_split(x0), y1 = f2_split(x1);
+                                const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                                if constexpr (kQuant) {
+                                    const float4 rv = *reinterpret_cast<const float4 *>(scales + 2 * BN + col0 + c0 + c);
+                                    sum2[0] = fma2(f2(p0, p1), f2(rv.x, rv.y), sum2[0]);
+                                    sum2[1] = fma2(f2(p2, p3), f2(rv.z, rv.w), sum2[1]);
+                                    p[c / 2] = f16_pack(p0, p1), p[c / 2 + 1] = f16_pack(p2, p3);
+                                } else {
+                                    sum2[0] = add2(sum2[0], f2(p0, p1));
+                                    sum2[1] = add2(sum2[1], f2(p2, p3));
+                                    p[c / 2] = bf16_pack(p0, p1), p[c / 2 + 1] = bf16_pack(p2, p3);
                                 }
                             }
-                            tmem_st_32x32b_x16(s_addr + 16 * i, p);
+                            tmem_st_32x32b_x16(s_addr + (col0 + c0) / 2, p);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        const float2 sums = f2_split(add2(sum2[0], sum2[1]));
+                        l += sums.x + sums.y;
                         tmem_wait_st();
                     }
                     if constexpr (!kQuant) {
                         // rows of V that no row of the item sees may hold anything: 0 * NaN must not happen
                         if (s == 0 && (t0 < g.item.lo || t0 + BN > g.item.hi)) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(ring_full(vr.slot), vr.phase, abort_flag));
+                            ok = __all_sync(0xffffffffu, mbar_wait(ring_full(vr.slot, 0), vr.phase, abort_flag));
                             if (!ok)
                                 break;
                             if (t0 + row < g.item.lo || t0 + row >= g.item.hi) {
@@ -789,64 +878,101 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             }
             if (!ok)
                 break;
-            // the next item's queries go in while the last product of this one runs
+            const int tok = g.start + g.item.tok0 + s * a.tpm + rt;
+            const int head = g.kvh * a.group + gi;
+            const bool whole = g.first && g.last;
+            const int slot = 2 * cta + (g.u != cta * units / grid ? 1 : 0);
+            const long long part = static_cast<long long>(slot) * (QT * BM) + s * BM + trow;
+            uint16_t *dst = a.out.data + static_cast<long long>(tok) * a.out.token_stride +
+                            static_cast<long long>(head) * a.out.head_stride;
             if (lane == 0)
                 ww.have[which ^ 1] = ww.walk.next(a, ww.seg[which ^ 1]);
             __syncwarp();
-            if (ww.have[which ^ 1] && active(ww.seg[which ^ 1]))
+            // the next item's queries go in while the last product of this one runs; with copies to
+            // add up their place is needed first
+            if (FOLD == 1 && ww.have[which ^ 1] && active(ww.seg[which ^ 1]))
                 load_q(ww.seg[which ^ 1]);
             if (act) {
                 ok = __all_sync(0xffffffffu, mbar_wait(pv_done(s), (cnt - 1) & 1, abort_flag));
                 if (!ok)
                     break;
                 tc_fence_after();
-                const int tok = g.start + g.item.tok0 + s * a.tpm + rt;
-                const int head = g.kvh * a.group + gi;
-                const bool whole = g.first && g.last;
-                const int slot = 2 * cta + (g.u != cta * units / grid ? 1 : 0);
-                if (whole) {
-                    const float inv = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;
-                    uint16_t *dst = a.out.data + static_cast<long long>(tok) * a.out.token_stride +
-                                    static_cast<long long>(head) * a.out.head_stride;
-                    if (warp_live) {
+                float weight = 1.f;
+                if constexpr (FOLD > 1) {
+                    // the copies' common maximum; each copy's weight; the sum of their sums
+                    float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold);
+                    ml[row] = make_float2(m * sl2, l);
+                    ok = fold_sync();
+                    if (!ok)
+                        break;
+                    float top = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < DP; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
-                            tmem_wait_ld(o);
-                            if (live) {
+                    for (int f = 0; f < FOLD; ++f)
+                        top = fmaxf(top, ml[f * kRows + trow].x);
+                    const float b = top == -INFINITY ? 0.f : top;
+                    weight = exp2f(m * sl2 - b);
+                    l = 0.f;
 #pragma unroll
-                                for (int k = 0; k < 32; k += 8)
-                                    if (c + k < dim)
-                                        *reinterpret_cast<uint4 *>(dst + c + k) = make_uint4(
-                                            bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
-                                            bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
-                                            bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
-                                            bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
-                            }
-                        }
+                    for (int f = 0; f < FOLD; ++f) {
+                        const float2 x = ml[f * kRows + trow];
+                        // in one power, as in the combine kernel
+                        l += x.y > 0.f ? exp2f(x.x - b + log2f(x.y)) : x.y == 0.f ? 0.f : x.y;
                     }
-                    if (live && a.lse)
-                        a.lse[static_cast<long long>(tok) * a.q.heads + head] =
-                            (m * sl2 + log2f(l)) * 0.69314718055994530942f;
-                } else if (warp_live) {
-                    const long long at = static_cast<long long>(slot) * (QT * BM) + s * BM + row;
-                    float *dst = a.part_o + at * dim;
+                    m = top;
+                } else {
+                    m *= sl2;
+                }
+                const float inv = whole ? (l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l) : 1.f;
+                if (warp_live || FOLD > 1) {
 #pragma unroll
                     for (int c = 0; c < DP; c += 32) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
                         tmem_wait_ld(o);
-                        if (live) {
+                        constexpr int kPer = 32 / FOLD;  // elements of the 32 that this thread writes
+                        int k0 = 0;
+                        if constexpr (FOLD > 1) {
+                            // through shared memory (the queries' place, read by now): rows of 32 words,
+                            // word k of row r at k ^ (r mod 32)
+                            float *x = reinterpret_cast<float *>(smem + lay.q);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4)
-                                if (c + k < dim)
-                                    *reinterpret_cast<uint4 *>(dst + c + k) =
+                            for (int k = 0; k < 32; ++k)
+                                x[row * 32 + (k ^ lane)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
+                            ok = ok && fold_sync();
+                            k0 = row / kRows * kPer;
+#pragma unroll
+                            for (int k = 0; k < kPer; ++k) {
+                                float sum = 0.f;
+#pragma unroll
+                                for (int f = 0; f < FOLD; ++f)
+                                    sum += x[(f * kRows + trow) * 32 + ((k0 + k) ^ lane)];
+                                o[k] = __float_as_uint(sum);
+                            }
+                            ok = ok && fold_sync();
+                        }
+                        if (live && whole) {
+#pragma unroll
+                            for (int k = 0; k < kPer; k += 8)
+                                if (c + k0 + k < dim)
+                                    *reinterpret_cast<uint4 *>(dst + c + k0 + k) = make_uint4(
+                                        bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+                                        bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+                                        bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+                                        bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+                        } else if (live) {
+#pragma unroll
+                            for (int k = 0; k < kPer; k += 4)
+                                if (c + k0 + k < dim)
+                                    *reinterpret_cast<uint4 *>(a.part_o + part * dim + c + k0 + k) =
                                         make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                         }
                     }
-                    if (live)
-                        a.part_ml[at] = make_float2(m * sl2, l);
+                }
+                if (live && col0 == 0) {
+                    if (!whole)
+                        a.part_ml[part] = make_float2(m, l);
+                    else if (a.lse)
+                        a.lse[static_cast<long long>(tok) * a.q.heads + head] = (m + log2f(l)) * 0.69314718055994530942f;
                 }
                 if (s == 0 && row == 0 && g.first && !g.last) {
                     const long long end = g.u + g.item.tiles - 1;  // the item's last unit
@@ -863,112 +989,128 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 }
                 tc_fence_before();
             }
+            if (FOLD > 1 && ok && ww.have[which ^ 1])
+                load_q(ww.seg[which ^ 1]);
             __syncwarp();  // the other lanes are done with this segment before lane 0 writes over it
         }
     } else {
         // -------------------------------------------------------------------- 8-bit codes to f16
         if constexpr (kQuant) {
             reg_dec<Shape<QT, TYPE>::kWideRegs>();
-            const int t = threadIdx.x - 128 * (1 + QT);
+            const int kv = warp >= 8 + 4 * QT ? 1 : 0;
+            const int t = threadIdx.x & 127;
             const int ps = a.cache.page_size, dim = a.cache.dim;
             constexpr int kChunks = DP / 16;
             Walk w;
             w.begin(a, prefix, units, grid, cta);
             Segment g;
-            int slot = 0, wslot = 0, tcnt = 0;
-            uint32_t phase = 0, wphase = 0;
+            int tcnt = 0;
+            // operand `item` (2 j for tile j's K, 2 j + 1 for its V) is in slot item mod size of a ring
+            int item = kv;
             bool ok = true;
             while (ok && w.next(a, g)) {
                 const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
-                // this thread's key of a tile: its two scales
-                auto scales_of = [&](int tile) {
-                    const int tok = tile * BN + t;
+                // this thread's key of a tile: its page, then (a tile later) its two scales
+                auto page_of = [&](int j) {
+                    const int tok = (g.tile + j) * BN + t;
+                    return j < g.tiles && tok >= g.item.lo && tok < g.item.hi ? __ldg(pt + tok / ps) : -1;
+                };
+                auto scales_of = [&](int j, int page) {
+                    const int tok = (g.tile + j) * BN + t;
                     float2 r = make_float2(0.f, -1.f);  // no key there
-                    if (tok >= g.item.lo && tok < g.item.hi) {
-                        const int page = min(max(__ldg(pt + tok / ps), 0), a.cache.pages - 1);
+                    if (j < g.tiles && tok >= g.item.lo && tok < g.item.hi) {
+                        page = min(max(page, 0), a.cache.pages - 1);
                         const long long at = (static_cast<long long>(page) * a.cache.heads + g.kvh) * ps + tok % ps;
-                        r = make_float2(a.cache.k_scale[at], a.cache.v_scale[at]);
+                        r = make_float2(__ldg(a.cache.k_scale + at), __ldg(a.cache.v_scale + at));
                     }
                     return r;
                 };
-                float2 sc = scales_of(g.tile);
+                float2 sc = kv == 0 ? scales_of(0, page_of(0)) : make_float2(0.f, 0.f);
+                int page = kv == 0 ? page_of(1) : 0;
                 float top_lv = -INFINITY;  // this thread's largest log2 of a value scale in the segment
                 for (int j = 0; j < g.tiles && ok; ++j) {
                     const int t0 = (g.tile + j) * BN;
-                    const float2 next_sc = j + 1 < g.tiles ? scales_of(g.tile + j + 1) : sc;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(wide_empty(wslot), wphase ^ 1u, abort_flag));
-                        if (!ok)
-                            break;
-                        if (kv == 0) {
-                            // the slot's last reader, the softmax two tiles back, is done: this wide
-                            // slot held that tile's V or a later operand
-                            float *sm = reinterpret_cast<float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
-                            float lv = sc.y > 0.f ? log2f(sc.y) : sc.y == 0.f ? -INFINITY : sc.y;
-                            float rv = sc.y != 0.f ? __fdiv_rn(1.f, sc.y) : 0.f;
-                            if (sc.y > 0.f)
-                                top_lv = fmaxf(top_lv, lv);
-                            if (__any_sync(0xffffffffu, sc.y == 0.f)) {
-                                // A row of zeros adds to l alone; any scale serves its codes.  One 2^60
-                                // below the largest seen keeps it from setting m' (P' of the others would
-                                // fall out of f16) and its own P' far above float32's least.
-                                float ref = top_lv;
-                                for (int o = 16; o > 0; o >>= 1)
-                                    ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-                                if (sc.y == 0.f) {
-                                    lv = fmaxf(floorf(ref) - 60.f, kLeastScale);
-                                    rv = exp2f(-lv);
-                                }
+                    float2 next_sc = sc;
+                    if (kv == 0) {
+                        next_sc = scales_of(j + 1, page);
+                        page = page_of(j + 2);
+                    }
+                    const int wslot = item % WIDE_RING, rslot = item % a.ring;
+                    // the n-th time (from 0) that this warpgroup takes over the slot, -1: it was free
+                    const int turn = item / (2 * WIDE_RING) - (kv == 0 ? wslot != 1 : wslot == 1);
+                    if (turn >= 0)
+                        ok = __all_sync(0xffffffffu, mbar_wait(wide_empty(wslot, kv), turn & 1, abort_flag));
+                    if (!ok)
+                        break;
+                    if (kv == 0) {
+                        // the slot's last reader, the softmax two tiles back, is done: this wide
+                        // slot held that tile's V or a later operand
+                        float *sm = reinterpret_cast<float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
+                        float lv = sc.y > 0.f ? __log2f(sc.y) : sc.y == 0.f ? -INFINITY : sc.y;
+                        float rv = sc.y != 0.f ? __frcp_rn(sc.y) : 0.f;
+                        if (sc.y > 0.f)
+                            top_lv = fmaxf(top_lv, lv);
+                        if (__any_sync(0xffffffffu, sc.y == 0.f)) {
+                            // A row of zeros adds to l alone; any scale serves its codes.  One 2^60
+                            // below the largest seen keeps it from setting m' (P' of the others would
+                            // fall out of f16) and its own P' far above float32's least.
+                            float ref = top_lv;
+                            for (int o = 16; o > 0; o >>= 1)
+                                ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+                            if (sc.y == 0.f) {
+                                lv = fmaxf(floorf(ref) - 60.f, kLeastScale);
+                                rv = exp2f(-lv);
                             }
-                            sm[t] = sc.x;
-                            sm[BN + t] = lv;
-                            sm[2 * BN + t] = rv;
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(scale_full(tcnt & 1));
                         }
-                        ok = __all_sync(0xffffffffu, mbar_wait(ring_full(slot), phase, abort_flag));
-                        if (!ok)
-                            break;
-                        const uint8_t *src = smem + lay.ring + slot * lay.ring_stage;
-                        uint8_t *dst = smem + lay.wide + wslot * kTile;
+                        sm[t] = sc.x;
+                        sm[BN + t] = lv;
+                        sm[2 * BN + t] = rv;
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(scale_full(tcnt & 1));
+                    }
+                    const uint32_t r_phase = (item / a.ring) >> (a.ring & 1) & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(ring_full(rslot, kv), r_phase, abort_flag));
+                    if (!ok)
+                        break;
+                    const uint8_t *src = smem + lay.ring + rslot * lay.ring_stage;
+                    uint8_t *dst = smem + lay.wide + wslot * kTile;
+                    // sixteen codes at a time; a code of zero is the number zero in both types
+                    uint4 v[kChunks];
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int r = i * (128 / kChunks) + t / kChunks, c = t % kChunks;
+                        v[i] = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
+                    }
+                    const int c = t % kChunks, odd = c >> 2, c0 = 2 * (c & 3);
+                    if (t0 < g.item.lo || t0 + BN > g.item.hi || c * 16 >= dim) {
 #pragma unroll
                         for (int i = 0; i < kChunks; ++i) {
-                            const int at = i * 128 + t, r = at / kChunks, c = at % kChunks;
-                            const bool in = c * 16 < dim && t0 + r >= g.item.lo && t0 + r < g.item.hi;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            uint4 lo4 = v, hi4 = v;
-                            if (in) {
-                                v = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
-                                const uint2 w0 = widen4<TYPE>(v.x), w1 = widen4<TYPE>(v.y), w2 = widen4<TYPE>(v.z),
-                                            w3 = widen4<TYPE>(v.w);
-                                lo4 = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                                hi4 = make_uint4(w2.x, w2.y, w3.x, w3.y);
-                            }
-                            // lanes of the two halves write opposite chunks of a pair, so eight lanes
-                            // cover all banks
-                            const int odd = c >> 2;
-                            uint8_t *d = dst + (c >> 2) * HALF_BYTES + r * 128;
-                            const int c0 = 2 * (c & 3);
-                            *reinterpret_cast<uint4 *>(d + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? hi4 : lo4;
-                            *reinterpret_cast<uint4 *>(d + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo4 : hi4;
-                        }
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(ring_empty(slot));
-                            mbar_arrive(wide_full(wslot));
-                        }
-                        if (++slot == a.ring) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
-                        if (++wslot == WIDE_RING) {
-                            wslot = 0;
-                            wphase ^= 1u;
+                            const int r = i * (128 / kChunks) + t / kChunks;
+                            if (t0 + r < g.item.lo || t0 + r >= g.item.hi || c * 16 >= dim)
+                                v[i] = make_uint4(0, 0, 0, 0);
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i) {
+                        const int r = i * (128 / kChunks) + t / kChunks;
+                        // lanes of the two halves write opposite chunks of a pair, so eight lanes
+                        // cover all banks
+                        const uint2 w0 = widen4<TYPE>(odd ? v[i].z : v[i].x), w1 = widen4<TYPE>(odd ? v[i].w : v[i].y),
+                                    w2 = widen4<TYPE>(odd ? v[i].x : v[i].z), w3 = widen4<TYPE>(odd ? v[i].y : v[i].w);
+                        uint8_t *d = dst + odd * HALF_BYTES + r * 128;
+                        *reinterpret_cast<uint4 *>(d + (((c0 + odd) ^ (r & 7)) << 4)) =
+                            make_uint4(w0.x, w0.y, w1.x, w1.y);
+                        *reinterpret_cast<uint4 *>(d + (((c0 + 1 - odd) ^ (r & 7)) << 4)) =
+                            make_uint4(w2.x, w2.y, w3.x, w3.y);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(ring_empty(rslot));
+                        mbar_arrive(wide_full(wslot));
+                    }
+                    item += 2;
                     sc = next_sc;
                     ++tcnt;
                 }
@@ -1055,6 +1197,16 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a)
 // Row tiles an item has: two when some sequence may have more rows than one holds.
 int row_tiles(const TokenBatch &t, int group) { return t.max_new > BM / group ? 2 : 1; }
 
+// Copies of the rows in a tile: with an 8-bit cache as many as fit.  A bf16 tile takes twice as long
+// to arrive, which hides the softmax of one copy, and adding copies up costs at the item's end.
+int row_copies(const PagedCache &c, const TokenBatch &t, int group)
+{
+    if (c.type == 0)
+        return 1;
+    const long long rows = static_cast<long long>(t.max_new) * group;
+    return rows <= BM / 4 ? 4 : rows <= BM / 2 ? 2 : 1;
+}
+
 struct Scratch {
     size_t records, ml, o, bytes;
 };
@@ -1092,7 +1244,7 @@ cudaError_t encode_cache(CUtensorMap *map, const PagedCache &c, const void *base
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int DP, int QT, int TYPE>
+template <int DP, int QT, int TYPE, int FOLD>
 cudaError_t launch(Args a, int sms, cudaStream_t stream)
 {
     a.ring = MAX_RING;
@@ -1106,21 +1258,33 @@ cudaError_t launch(Args a, int sms, cudaStream_t stream)
     if ((e = encode_cache(&mk, a.cache, a.cache.k, a.box)) != cudaSuccess ||
         (e = encode_cache(&mv, a.cache, a.cache.v, a.box)) != cudaSuccess)
         return e;
-    auto kern = attention_kernel<DP, QT, TYPE>;
+    auto kern = attention_kernel<DP, QT, TYPE, FOLD>;
     if ((e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem)) != cudaSuccess)
         return e;
     return launch_dependent(kern, dim3(static_cast<unsigned>(sms)), dim3(Shape<QT, TYPE>::kThreads),
                             static_cast<size_t>(smem), stream, mk, mv, a);
 }
 
-template <int DP, int QT>
+template <int DP, int QT, int FOLD>
 cudaError_t launch_type(const Args &a, int sms, cudaStream_t stream)
 {
     switch (a.cache.type) {
-    case 0: return launch<DP, QT, 0>(a, sms, stream);
-    case 1: return launch<DP, QT, 1>(a, sms, stream);
-    default: return launch<DP, QT, 2>(a, sms, stream);
+    case 0: return launch<DP, QT, 0, FOLD>(a, sms, stream);
+    case 1: return launch<DP, QT, 1, FOLD>(a, sms, stream);
+    default: return launch<DP, QT, 2, FOLD>(a, sms, stream);
     }
+}
+
+template <int DP>
+cudaError_t launch_rows(const Args &a, int tiles, int fold, int sms, cudaStream_t stream)
+{
+    if (tiles == 2)
+        return launch_type<DP, 2, 1>(a, sms, stream);
+    if (fold == 4)
+        return a.cache.type == 1 ? launch<DP, 1, 1, 4>(a, sms, stream) : launch<DP, 1, 2, 4>(a, sms, stream);
+    if (fold == 2)
+        return a.cache.type == 1 ? launch<DP, 1, 1, 2>(a, sms, stream) : launch<DP, 1, 2, 2>(a, sms, stream);
+    return launch_type<DP, 1, 1>(a, sms, stream);
 }
 
 }  // namespace
@@ -1149,7 +1313,8 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     a.window = opt.window >= tokens.max_pages * cache.page_size ? 0 : opt.window;
     a.group = q.heads / cache.heads;
     const int tiles = row_tiles(tokens, a.group);
-    a.tpm = BM / a.group;
+    const int fold = row_copies(cache, tokens, a.group);
+    a.tpm = BM / fold / a.group;
     a.span = tiles * a.tpm;
     a.box = std::gcd(cache.page_size, BN);
     a.status = status;
@@ -1159,10 +1324,7 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     a.part_ml = reinterpret_cast<float2 *>(p + s.ml);
     a.part_o = reinterpret_cast<float *>(p + s.o);
     cudaError_t e;
-    if (cache.dim <= 64)
-        e = tiles == 1 ? launch_type<64, 1>(a, sms, stream) : launch_type<64, 2>(a, sms, stream);
-    else
-        e = tiles == 1 ? launch_type<128, 1>(a, sms, stream) : launch_type<128, 2>(a, sms, stream);
+    e = cache.dim <= 64 ? launch_rows<64>(a, tiles, fold, sms, stream) : launch_rows<128>(a, tiles, fold, sms, stream);
     if (e != cudaSuccess)
         return e;
     CombineArgs c{};

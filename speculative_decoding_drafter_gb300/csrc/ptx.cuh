@@ -245,6 +245,28 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t 
     return d;
 }
 
+// One lane of a converged warp (the same one each time); the compiler then knows that what the
+// branch issues comes from one thread with warp-uniform operands.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
+}
+
+// The low and the (constant) high word of a descriptor; adding bytes >> 4 to the low word moves
+// the start address.
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]: A's rows are the lanes, two consecutive 16-bit K elements a
 // 32-bit column.
 __device__ __forceinline__ void umma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
