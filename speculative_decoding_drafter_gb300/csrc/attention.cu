@@ -47,7 +47,9 @@ constexpr int BN = 128;  // keys of a tile
 constexpr int HALF_BYTES = 128 * 128;  // 128 rows of 64 16-bit elements
 constexpr int SMEM_LIMIT = 227 * 1024;
 constexpr int MAX_RING = 8;
-constexpr int WIDE_RING = 3;  // widened 8-bit tiles
+constexpr int MAX_WIDE = 4;
+constexpr int SEGMENTS = 4;  // segments that the walking warp may be ahead
+constexpr int SCALES = 4;  // tiles whose scales are held
 constexpr float kLeastScale = -108.f;  // log2 of the least scale a cache holds, 1e-30 / 448
 constexpr float LAZY = 8.f;   // how far the running maximum may lag, in powers of two
 
@@ -65,6 +67,7 @@ struct Args {
     int causal, window, group;
     int tpm;   // tokens of a row tile
     int span;  // tokens of an item
+    uint32_t page_magic, page_shift;  // token / page_size = umulhi(token, magic) >> shift
     int box;   // rows of a TMA box: gcd(page_size, 128)
     int ring;  // stages of the TMA ring
     SplitRecord *records;
@@ -76,6 +79,12 @@ struct Args {
 struct Sequence {
     int start, n, len;
 };
+
+// token / page_size for 0 <= token < 2^31.
+__device__ __forceinline__ int page_of_token(const Args &a, int token)
+{
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(token), a.page_magic) >> a.page_shift);
+}
 
 __device__ __forceinline__ Sequence sequence_at(const Args &a, int b)
 {
@@ -118,19 +127,22 @@ struct Segment {
     Item item;
     int b, kvh, start;   // start: the sequence's first packed token
     int tile, tiles;
-    long long u;         // units before it
-    bool first, last;    // has the item's first / last tile
+    int first, last;     // has the item's first / last tile
+    int slot;            // where a piece of an item goes
+    int end_cta;         // of an item that begins here and ends elsewhere: the CTA with its last tile
 };
 
 // The segments of a CTA's share [u, u_end) of the units (cache head by cache head, item by item).
+// One warp walks and hands the segments to the others through shared memory: walking code in every
+// role made the loops too long for the instruction cache (warps waited for instructions half the time).
 struct Walk {
-    long long u, u_end;
+    long long u, u_begin, u_end;
     int b, kvh, qt, off, nq;
     Sequence s;
 
     __device__ __forceinline__ void begin(const Args &a, const int *prefix, long long units, int grid, int c)
     {
-        u = c * units / grid;
+        u = u_begin = c * units / grid;
         u_end = (c + 1) * units / grid;
         int lo = 0, hi = a.tokens.B;  // the largest b with prefix[b] * heads <= u
         while (hi - lo > 1) {
@@ -155,10 +167,12 @@ struct Walk {
         }
     }
 
-    __device__ __forceinline__ bool next(const Args &a, Segment &g)
+    __device__ __forceinline__ bool next(const Args &a, int cta, long long units, int grid, Segment &g)
     {
-        if (u >= u_end)
+        if (u >= u_end) {
+            g.tiles = 0;
             return false;
+        }
         while (kvh == a.cache.heads) {  // the next sequence that has tokens
             ++b;
             s = sequence_at(a, b);
@@ -169,10 +183,11 @@ struct Walk {
         g.b = b;
         g.kvh = kvh;
         g.start = s.start;
-        g.u = u;
+        g.slot = 2 * cta + (u != u_begin ? 1 : 0);
         g.tile = g.item.tile0 + off;
         g.tiles = static_cast<int>(min(static_cast<long long>(g.item.tiles - off), u_end - u));
         g.first = off == 0;
+        g.end_cta = static_cast<int>(((u - off + g.item.tiles) * grid - 1) / units);
         u += g.tiles;
         off += g.tiles;
         g.last = off == g.item.tiles;
@@ -235,46 +250,42 @@ __device__ __forceinline__ uint2 widen4(uint32_t w)
 
 template <int QT, int TYPE>
 struct Shape {
+    // widened tiles: two K and two V; with two row tiles there is room for three in rotation
+    static constexpr int kWideRing = QT == 1 ? 4 : 3;
     static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 2 : 0));
     // registers of a thread after the roles part: control, softmax, widening (their sum times 128
     // is at most what the launch holds: 65536 / threads, a multiple of 8, times the threads)
-    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 144 : 216;
-    static constexpr int kWideRegs = QT == 2 ? 64 : 104;
-    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 64 : 88;
+    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 128 : 184;
+    static constexpr int kWideRegs = QT == 2 ? 72 : 112;
+    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 80 : 104;
     static constexpr bool kSplitRegs = kThreads > 256;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static_assert(!kSplitRegs || kControlRegs + QT * kSoftRegs + (TYPE ? 2 * kWideRegs : 0) <=
                                      kThreads / 128 * kLaunchRegs, "setmaxnreg.inc would wait forever");
 };
 
-// A softmax warp's walk, kept in shared memory: its registers hold a row of scores.
-struct WarpWalk {
-    Walk walk;
-    Segment seg[2];
-    int have[2];
-};
-
-// Shared memory: Q tiles | TMA ring | widened ring (8-bit) | scales (8-bit) | copies' (m, l) | barriers | walks | prefix sums.
+// Shared memory: Q tiles (two row tiles; one tile's queries are in TMEM) | TMA ring | widened ring
+// (8-bit) | scales (8-bit) | place to add copies up, their (m, l) | barriers | segments | prefix sums.
 struct Layout {
-    int q, ring, ring_stage, wide, scales, fold, bars, walks, prefix, bytes;
+    int q, ring, ring_stage, wide, scales, fold, bars, segs, prefix, bytes;
 };
 
-constexpr int BAR_COUNT = 3 * MAX_RING + 3 * WIDE_RING + 2 + 2 + 2 + 2 + 2 + 1 + 1;  // tmem slot and abort flag follow
+constexpr int BAR_COUNT = 3 * MAX_RING + 3 * MAX_WIDE + 2 + 2 + 2 + 2 + SCALES + 1 + 1 + 2 + 2 * SEGMENTS;  // tmem slot and abort flag follow
 
-template <int DP, int QT, int TYPE>
+template <int DP, int QT, int TYPE, int FOLD>
 __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
 {
     Layout l{};
     const int tile = DP / 64 * HALF_BYTES;
     l.q = 0;
-    l.ring = QT * tile;
+    l.ring = QT == 2 ? QT * tile : 0;
     l.ring_stage = TYPE ? 128 * dim : tile;
     l.wide = l.ring + ring * l.ring_stage;
-    l.scales = l.wide + (TYPE ? WIDE_RING * tile : 0);
-    l.fold = l.scales + (TYPE ? 2 * 3 * BN * 4 : 0);
-    l.bars = l.fold + (QT == 1 ? BM * 8 : 0);
-    l.walks = l.bars + BAR_COUNT * 8 + 8;
-    l.prefix = l.walks + 4 * QT * static_cast<int>(sizeof(WarpWalk));
+    l.scales = l.wide + (TYPE ? Shape<QT, TYPE>::kWideRing * tile : 0);
+    l.fold = l.scales + (TYPE ? SCALES * 3 * BN * 4 : 0);
+    l.bars = l.fold + (FOLD > 1 ? BM * 32 * 4 + BM * 8 : 0);
+    l.segs = l.bars + BAR_COUNT * 8 + 8;
+    l.prefix = l.segs + SEGMENTS * static_cast<int>(sizeof(Segment));
     l.bytes = l.prefix + (B + 1) * 4;
     return l;
 }
@@ -287,16 +298,13 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity)
             return;
 }
 
-// N consecutive columns of this thread's lane, all in flight before the wait.
-template <int N>
-__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&v)[N])
+// 16 bytes of shared memory.  volatile keeps a batch of them together and ahead of the wait that
+// follows: behind the widening warps' stores each takes some 250 cycles, so they must all be in flight.
+__device__ __forceinline__ float4 lds4(uint32_t addr)
 {
-#pragma unroll
-    for (int i = 0; i < N; i += 32)
-        tmem_ld_32x32b_x32(taddr + i, reinterpret_cast<uint32_t(&)[32]>(v[i]));
-#pragma unroll
-    for (int i = 0; i < N; i += 32)
-        tmem_wait_ld(reinterpret_cast<uint32_t(&)[32]>(v[i]));
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
 }
 
 __device__ __forceinline__ uint64_t load2(const uint32_t *v) { return f2(__uint_as_float(v[0]), __uint_as_float(v[1])); }
@@ -306,6 +314,17 @@ __device__ __forceinline__ void store2(uint32_t *v, uint64_t x)
     const float2 f = f2_split(x);
     v[0] = __float_as_uint(f.x);
     v[1] = __float_as_uint(f.y);
+}
+
+__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
+// A converged warp's wait; what has to poll does so out of line.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag);
 }
 
 template <int N>
@@ -321,17 +340,22 @@ __device__ __forceinline__ void reg_inc()
 
 template <int DP, int QT, int TYPE, int FOLD>
 __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
-    attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Args a)
+    attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ Args a)
 {
     constexpr int kThreads = Shape<QT, TYPE>::kThreads;
     constexpr int kHalves = DP / 64;
     constexpr int kTile = kHalves * HALF_BYTES;
     constexpr bool kQuant = TYPE != 0;
+    constexpr int kWide = Shape<QT, TYPE>::kWideRing;
     constexpr int kRows = BM / FOLD;  // distinct rows of a tile
     constexpr int kCols = BN / FOLD;  // keys of a tile that a thread takes
+    constexpr int kQCol = 384;        // TMEM: two S at 0 and 128, O at 256 (and 384), one tile's Q at 384
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const Layout lay = layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B);
+    // an offset into the array, not a rounded address: the compiler must see shared memory, or every
+    // access becomes a generic one (the scales' reads were the longest step of a tile)
+    uint8_t *smem = smem_raw + (1024u - (smem_u32(smem_raw) & 1023u)) % 1024u;
+    const Layout lay = layout_of<DP, QT, TYPE, FOLD>(a.ring, a.cache.dim, a.tokens.B);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + lay.bars;
     // A barrier's phases are told apart by parity, so whoever waits on one must wait for every phase
@@ -340,20 +364,23 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     auto ring_full = [&](int s, int kv) { return bar0 + 8u * (s + (kQuant ? kv * MAX_RING : 0)); };
     auto ring_empty = [&](int s) { return bar0 + 8u * (2 * MAX_RING + s); };
     auto wide_full = [&](int s) { return bar0 + 8u * (3 * MAX_RING + s); };
-    auto wide_empty = [&](int s, int next_kv) { return bar0 + 8u * (3 * MAX_RING + WIDE_RING * (1 + next_kv) + s); };
-    constexpr int kRest = 3 * MAX_RING + 3 * WIDE_RING;
+    auto wide_empty = [&](int s, int next_kv) { return bar0 + 8u * (3 * MAX_RING + MAX_WIDE * (1 + next_kv) + s); };
+    constexpr int kRest = 3 * MAX_RING + 3 * MAX_WIDE;
     auto s_full = [&](int x) { return bar0 + 8u * (kRest + x); };
     auto p_full = [&](int x) { return bar0 + 8u * (kRest + 2 + x); };
     auto pv_done = [&](int s) { return bar0 + 8u * (kRest + 4 + s); };
     auto q_full = [&](int s) { return bar0 + 8u * (kRest + 6 + s); };
     auto scale_full = [&](int s) { return bar0 + 8u * (kRest + 8 + s); };
-    const uint32_t drain_bar = bar0 + 8u * (kRest + 10);
-    const uint32_t fold_bar = bar0 + 8u * (kRest + 11);
+    const uint32_t drain_bar = bar0 + 8u * (kRest + 8 + SCALES);
+    const uint32_t fold_bar = bar0 + 8u * (kRest + 9 + SCALES);
+    auto soft_done = [&](int x) { return bar0 + 8u * (kRest + 10 + SCALES + x); };
+    auto seg_full = [&](int i) { return bar0 + 8u * (kRest + 12 + SCALES + i); };
+    auto seg_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + SCALES + SEGMENTS + i); };
     // what the MMAs read: the TMA ring itself, or the widened one
-    const int op_size = kQuant ? WIDE_RING : a.ring;
+    const int op_size = kQuant ? kWide : a.ring;
     const uint32_t op_base = sbase + (kQuant ? lay.wide : lay.ring);
     auto op_full = [&](int s) { return kQuant ? wide_full(s) : ring_full(s, 0); };
-    auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, 1 - kv) : ring_empty(s); };
+    auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, kWide % 2 ? 1 - kv : kv) : ring_empty(s); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.bars + BAR_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
@@ -367,7 +394,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 mbar_init(ring_full(s, 1), 1);
             mbar_init(ring_empty(s), kQuant ? 4 : 1);
         }
-        for (int s = 0; s < WIDE_RING; ++s) {
+        for (int s = 0; s < kWide; ++s) {
             mbar_init(wide_full(s), 4);
             mbar_init(wide_empty(s, 0), 1);
             mbar_init(wide_empty(s, 1), 1);
@@ -377,7 +404,13 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_init(p_full(s), 4);
             mbar_init(pv_done(s), 1);
             mbar_init(q_full(s), 4);
-            mbar_init(scale_full(s), 4);
+            mbar_init(soft_done(s), 4);
+        }
+        for (int s = 0; s < SCALES; ++s)
+            mbar_init(scale_full(s), 1);
+        for (int s = 0; s < SEGMENTS; ++s) {
+            mbar_init(seg_full(s), 1);
+            mbar_init(seg_empty(s), 1 + 4 * QT + (kQuant ? 2 + 8 : 0));  // warps that read it
         }
         mbar_init(drain_bar, 1);
         mbar_init(fold_bar, 4);
@@ -441,6 +474,14 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), units));
     const int cta = blockIdx.x;
     const bool works = cta < grid;
+    Segment *segs = reinterpret_cast<Segment *>(smem + lay.segs);
+    // the CTA's n-th segment (tiles == 0: there is none), and done with it
+    auto seg_wait = [&](int n) { return warp_wait(seg_full(n % SEGMENTS), (n / SEGMENTS) & 1, abort_flag); };
+    auto seg_done = [&](int n) {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(seg_empty(n % SEGMENTS));
+    };
 
     if (!works) {
         if (threadIdx.x == 0)
@@ -449,8 +490,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         // ---------------------------------------------------------------- TMA producer
         if constexpr (Shape<QT, TYPE>::kSplitRegs)
             reg_dec<Shape<QT, TYPE>::kControlRegs>();
-        Walk w;
-        w.begin(a, prefix, units, grid, cta);
+        Walk walk;
+        walk.begin(a, prefix, units, grid, cta);
         Segment g;
         const int boxes = BN / a.box;
         const int ps = a.cache.page_size, dim = a.cache.dim;
@@ -459,12 +500,24 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true;
-        while (ok && w.next(a, g)) {
+        for (int n = 0; ok; ++n) {
+            if (n >= SEGMENTS)
+                ok = warp_wait(seg_empty(n % SEGMENTS), (n / SEGMENTS - 1) & 1, abort_flag);
+            if (!ok)
+                break;
+            const bool have = walk.next(a, cta, units, grid, g);
+            if (lane == 0) {
+                segs[n % SEGMENTS] = g;
+                mbar_arrive(seg_full(n % SEGMENTS));
+            }
+            __syncwarp();
+            if (!have)
+                break;
             const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
             auto page_of = [&](int tile) {
                 const int tok = tile * BN + lane * a.box;
                 const bool need = lane < boxes && tok < g.item.hi && tok + a.box > g.item.lo;
-                return need ? min(max(__ldg(pt + tok / ps), 0), a.cache.pages - 1) : -1;
+                return need ? min(max(__ldg(pt + page_of_token(a, tok)), 0), a.cache.pages - 1) : -1;
             };
             int page = page_of(g.tile);
             for (int j = 0; j < g.tiles && ok; ++j) {
@@ -473,22 +526,23 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(ring_empty(slot), phase ^ 1u, abort_flag));
+                    ok = warp_wait(ring_empty(slot), phase ^ 1u, abort_flag);
                     if (!ok)
                         break;
                     if (lane == 0)
                         mbar_arrive_expect_tx(ring_full(slot, kv), bytes);
                     __syncwarp();
                     if (page >= 0) {
+                        const int in_page = tok - page_of_token(a, tok) * ps;
                         const CUtensorMap *map = kv ? &map_v : &map_k;
                         const uint32_t dst = sbase + lay.ring + slot * lay.ring_stage;
                         if constexpr (kQuant) {
-                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot, kv), 0, tok % ps, g.kvh, page);
+                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot, kv), 0, in_page, g.kvh, page);
                         } else {
 #pragma unroll
                             for (int h = 0; h < kHalves; ++h)
                                 tma_load_4d(dst + h * HALF_BYTES + lane * a.box * 128, map, ring_full(slot, kv), h * 64,
-                                            tok % ps, g.kvh, page);
+                                            in_page, g.kvh, page);
                         }
                     }
                     __syncwarp();
@@ -520,9 +574,6 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             const uint64_t k_desc = sw128_kmajor_desc(0), v_desc = sw128_mnmajor_desc(0, HALF_BYTES);
             const uint32_t k_lo = static_cast<uint32_t>(k_desc), k_hi = static_cast<uint32_t>(k_desc >> 32);
             const uint32_t v_lo = static_cast<uint32_t>(v_desc), v_hi = static_cast<uint32_t>(v_desc >> 32);
-            Walk w;
-            w.begin(a, prefix, units, grid, cta);
-            Segment g;
             RingAt kr{0, 0}, vr{1, 0};
             int cnt[2] = {0, 0};  // tiles done, per row tile (QT = 2) or in all (QT = 1, cnt[0])
             uint32_t q_phase[2] = {0, 0};
@@ -535,7 +586,10 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < DP / 16; ++kk) {
                         const uint32_t o = ((kk / 4) * HALF_BYTES + (kk % 4) * 32) >> 4;
-                        umma_bf16(d, desc_at(q + o, k_hi), desc_at(k + o, k_hi), idesc_qk, kk > 0);
+                        if constexpr (QT == 1)
+                            umma_f16_tmem_a(d, tmem + kQCol + kk * 8, desc_at(k + o, k_hi), idesc_qk, kk > 0);
+                        else
+                            umma_bf16(d, desc_at(q + o, k_hi), desc_at(k + o, k_hi), idesc_qk, kk > 0);
                     }
                     umma_commit(s_full(sbuf));
                 }
@@ -560,11 +614,16 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 __syncwarp();
             };
 #define DF2_WAIT(bar, parity)                                               \
-    if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag))) { \
+    if (!warp_wait(bar, parity, abort_flag)) {                              \
         ok = false;                                                         \
         break;                                                              \
     }
-            while (ok && w.next(a, g)) {
+            for (int n = 0; ok; ++n) {
+                DF2_WAIT(seg_full(n % SEGMENTS), (n / SEGMENTS) & 1);
+                const Segment &g = segs[n % SEGMENTS];
+                const int tiles = g.tiles;
+                if (tiles == 0)
+                    break;
                 if constexpr (QT == 2) {
                     const int mt = g.item.ntok > a.tpm ? 2 : 1;
                     for (int s = 0; s < mt; ++s) {
@@ -579,8 +638,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         qk(s, s, kr.slot);
                     commit(op_empty(kr.slot, 0));
                     kr.step(op_size);
-                    for (int j = 0; j < g.tiles && ok; ++j) {
-                        const bool more = j + 1 < g.tiles;
+                    for (int j = 0; j < tiles && ok; ++j) {
+                        const bool more = j + 1 < tiles;
                         DF2_WAIT(op_full(vr.slot), vr.phase);
                         for (int s = 0; s < mt; ++s) {
                             DF2_WAIT(p_full(s), cnt[s] & 1);
@@ -607,13 +666,13 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     DF2_WAIT(q_full(0), q_phase[0]);
                     q_phase[0] ^= 1u;
                     DF2_WAIT(op_full(kr.slot), kr.phase);
-                    tc_fence_after();
+                    tc_fence_after();  // the queries in TMEM too
                     qk(0, cnt[0] & 1, kr.slot);
                     commit(op_empty(kr.slot, 0));
                     kr.step(op_size);
-                    for (int j = 0; j < g.tiles; ++j) {
+                    for (int j = 0; j < tiles; ++j) {
                         const int sbuf = cnt[0] & 1;
-                        if (j + 1 < g.tiles) {
+                        if (j + 1 < tiles) {
                             DF2_WAIT(op_full(kr.slot), kr.phase);
                             tc_fence_after();
                             qk(0, sbuf ^ 1, kr.slot);
@@ -629,11 +688,115 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         vr.step(op_size);
                     }
                 }
+                seg_done(n);
             }
 #undef DF2_WAIT
             // every MMA issued must finish before TMEM is released (in a healthy run all have)
             commit(drain_bar);
             drain_wait(drain_bar, 0);
+        } else if (kQuant && warp >= 2) {
+            // ------------------------------------------------------------ scales of the keys and values
+            // The two warps take alternate tiles, a lane four keys: their pages, a turn later their
+            // scales, a turn later into shared memory as (ks, log2 vs, 1 / vs).  Two sets of registers
+            // take turns, so a turn never waits for the loads it has just issued.
+            const int ps = a.cache.page_size;
+            int base = 0;  // tiles of the CTA before the segment
+            bool ok = true;
+            struct Turn {
+                int page[4];
+                float2 sc[4];
+            };
+            for (int n = 0; ok; ++n) {
+                ok = seg_wait(n);
+                if (!ok || segs[n % SEGMENTS].tiles == 0)
+                    break;
+                const Segment &g = segs[n % SEGMENTS];
+                const int tiles = g.tiles;
+                const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
+                auto held = [&](int j, int i) {
+                    const int tok = (g.tile + j) * BN + i * 32 + lane;
+                    return j < tiles && tok >= g.item.lo && tok < g.item.hi;
+                };
+                auto load_pages = [&](int j, Turn &t) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        t.page[i] = held(j, i) ? __ldg(pt + page_of_token(a, (g.tile + j) * BN + i * 32 + lane)) : -1;
+                };
+                auto load_scales = [&](int j, Turn &t) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        t.sc[i] = make_float2(0.f, -1.f);  // no key there
+                        if (held(j, i)) {
+                            const int tok = (g.tile + j) * BN + i * 32 + lane;
+                            const long long at = (static_cast<long long>(min(max(t.page[i], 0), a.cache.pages - 1)) *
+                                                      a.cache.heads + g.kvh) * ps + tok - page_of_token(a, tok) * ps;
+                            t.sc[i] = make_float2(__ldg(a.cache.k_scale + at), __ldg(a.cache.v_scale + at));
+                        }
+                    }
+                };
+                float top_lv = -INFINITY;  // this lane's largest log2 of a value scale in the segment
+                // tile j from `now`, whose scales are on their way; `then` has the pages of tile j + 2
+                auto turn = [&](int j, Turn &now, Turn &then) {
+                    load_scales(j + 2, then);
+                    load_pages(j + 4, now);
+                    float lv[4], rv[4];
+                    bool zero = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float vs = now.sc[i].y;
+                        lv[i] = vs > 0.f ? __log2f(vs) : vs == 0.f ? -INFINITY : vs;
+                        rv[i] = vs != 0.f ? __frcp_rn(vs) : 0.f;
+                        if (vs > 0.f)
+                            top_lv = fmaxf(top_lv, lv[i]);
+                        zero |= vs == 0.f;
+                    }
+                    if (__any_sync(0xffffffffu, zero)) {
+                        // A row of zeros adds to l alone; any scale serves its codes.  One 2^60 below
+                        // the largest seen keeps it from setting m' (P' of the others would fall out of
+                        // f16) and its own P' far above float32's least.
+                        float ref = top_lv;
+                        for (int o = 16; o > 0; o >>= 1)
+                            ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (now.sc[i].y == 0.f) {
+                                lv[i] = fmaxf(floorf(ref) - 60.f, kLeastScale);
+                                rv[i] = exp2f(-lv[i]);
+                            }
+                    }
+                    // the first softmax warpgroup is done with the tile two back, so the second (which
+                    // the order of the MMAs keeps less than two tiles behind) with the one four back,
+                    // whose place this is
+                    const int at = base + j;
+                    if (at >= 2)
+                        ok = warp_wait(soft_done(at & 1), ((at >> 1) - 1) & 1, abort_flag);
+                    if (!ok)
+                        return;
+                    float *sm = reinterpret_cast<float *>(smem + lay.scales) + (at % SCALES) * 3 * BN;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = i * 32 + lane;
+                        sm[k] = now.sc[i].x;
+                        sm[BN + k] = lv[i];
+                        sm[2 * BN + k] = rv[i];
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(scale_full(at % SCALES));
+                };
+                Turn x, y;
+                const int first = (warp ^ base) & 1;  // this warp's first tile of the segment
+                load_pages(first, x);
+                load_pages(first + 2, y);
+                load_scales(first, x);
+                for (int j = first; j < tiles && ok; j += 4) {
+                    turn(j, x, y);
+                    if (j + 2 < tiles && ok)
+                        turn(j + 2, y, x);
+                }
+                base += tiles;
+                seg_done(n);
+            }
         }
     } else if (warp < 4 + 4 * QT) {
         // -------------------------------------------------------------------- softmax, a thread per row
@@ -648,12 +811,6 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         const int gi = trow - rt * a.group;
         const bool in_tile = trow < a.tpm * a.group;
         const int dim = a.cache.dim;
-        WarpWalk &ww = reinterpret_cast<WarpWalk *>(smem + lay.walks)[warp - 4];
-        if (lane == 0) {
-            ww.walk.begin(a, prefix, units, grid, cta);
-            ww.have[0] = ww.walk.next(a, ww.seg[0]);
-        }
-        __syncwarp();
         RingAt vr{1, 0};
         int cnt = 0;   // tiles this warpgroup has done
         int tcnt = 0;  // tiles of the CTA
@@ -662,47 +819,53 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         if (s == 0 && row == 0)
             a.records[cta].valid = 0;
 
-        // Q row of a segment's item into shared memory (swizzled, K-major)
+        // Q row of a segment's item: into shared memory (swizzled, K-major), or with one row tile
+        // into TMEM, where it costs the MMAs no shared-memory reads
         auto active = [&](const Segment &x) { return s * a.tpm < x.item.ntok; };
         auto row_live = [&](const Segment &x) { return in_tile && s * a.tpm + rt < x.item.ntok; };
         auto load_q = [&](const Segment &x) {
-            if (row_live(x)) {
-                const uint16_t *src = a.q.data +
-                                      static_cast<long long>(x.start + x.item.tok0 + s * a.tpm + rt) * a.q.token_stride +
-                                      static_cast<long long>(x.kvh * a.group + gi) * a.q.head_stride;
+            const bool in = row_live(x);
+            uint32_t v[DP / 2];
+            const uint16_t *src = a.q.data +
+                                  static_cast<long long>(x.start + x.item.tok0 + s * a.tpm + rt) * a.q.token_stride +
+                                  static_cast<long long>(x.kvh * a.group + gi) * a.q.head_stride;
+#pragma unroll
+            for (int i = 0; i < DP / 8; ++i) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (in && 8 * i < dim)
+                    w = *reinterpret_cast<const uint4 *>(src + 8 * i);
+                v[4 * i] = w.x, v[4 * i + 1] = w.y, v[4 * i + 2] = w.z, v[4 * i + 3] = w.w;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < DP / 2; ++i) {
+                v[i] = (v[i] & a.q_and) ^ a.q_xor;
+                if constexpr (kQuant)
+                    top = __vmaxu2(top, v[i] & 0x7F807F80u);  // exponents
+            }
+            if constexpr (kQuant) {
+                const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // biased
+                const int shift = e == 0 ? 0 : min(14 - (e - 127), 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
+                next_qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+                for (int i = 0; i < DP / 2; ++i)
+                    v[i] = f16_pack(bf16_lo(v[i]) * up, bf16_hi(v[i]) * up);
+            }
+            if constexpr (QT == 1) {
+#pragma unroll
+                for (int i = 0; i < DP / 2; i += 32)
+                    tmem_st_32x32b_x32(lane_base + kQCol + i, reinterpret_cast<const uint32_t(&)[32]>(v[i]));
+                tmem_wait_st();
+                tc_fence_before();
+            } else {
                 uint8_t *dst = smem + lay.q + s * kTile + row * 128;
-                uint4 v[DP / 8];
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < DP / 8; ++i) {
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (8 * i < dim)
-                        v[i] = *reinterpret_cast<const uint4 *>(src + 8 * i);
-                    v[i].x = (v[i].x & a.q_and) ^ a.q_xor, v[i].y = (v[i].y & a.q_and) ^ a.q_xor;
-                    v[i].z = (v[i].z & a.q_and) ^ a.q_xor, v[i].w = (v[i].w & a.q_and) ^ a.q_xor;
-                    if constexpr (kQuant) {
-                        const uint32_t m = 0x7F807F80u;  // exponents
-                        top = __vmaxu2(__vmaxu2(top, v[i].x & m), __vmaxu2(v[i].y & m, __vmaxu2(v[i].z & m, v[i].w & m)));
-                    }
-                }
-                if constexpr (kQuant) {
-                    const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7);  // biased
-                    const int shift = e == 0 ? 0 : min(14 - (e - 127), 126);
-                    const float up = __uint_as_float(static_cast<uint32_t>(shift + 127) << 23);
-                    next_qscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
-#pragma unroll
-                    for (int i = 0; i < DP / 8; ++i) {
-                        v[i].x = f16_pack(bf16_lo(v[i].x) * up, bf16_hi(v[i].x) * up);
-                        v[i].y = f16_pack(bf16_lo(v[i].y) * up, bf16_hi(v[i].y) * up);
-                        v[i].z = f16_pack(bf16_lo(v[i].z) * up, bf16_hi(v[i].z) * up);
-                        v[i].w = f16_pack(bf16_lo(v[i].w) * up, bf16_hi(v[i].w) * up);
-                    }
-                }
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (i / 8) * HALF_BYTES + (((i & 7) ^ (row & 7)) << 4)) = v[i];
+                    *reinterpret_cast<uint4 *>(dst + (i / 8) * HALF_BYTES + (((i & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                fence_proxy_async();
             }
-            fence_proxy_async();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(q_full(s));
@@ -719,13 +882,14 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             return met;
         };
 
-        if (active(ww.seg[0]))
-            load_q(ww.seg[0]);
-        for (int which = 0; ok && ww.have[which]; which ^= 1) {
-            const Segment &g = ww.seg[which];
+        // Segment n after segment n; before the first there is only its queries to load.
+        bool more = true;
+        for (int n = -1; more; ++n) {
+            const Segment &g = segs[n & (SEGMENTS - 1)];
+            const bool started = n >= 0;
             qscale = next_qscale;
-            const bool act = active(g);
-            const bool live = row_live(g);
+            const bool act = started && active(g);
+            const bool live = started && row_live(g);
             const bool warp_live = __any_sync(0xffffffffu, live);
             // keys the row sees, relative to the segment's tiles
             int hi = 0x7FFFFFFF, lo = 0;  // rows of no token: whatever comes out goes nowhere
@@ -741,45 +905,85 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     const int t0 = (g.tile + j) * BN;
                     const int sbuf = QT == 2 ? s : cnt & 1;
                     const uint32_t s_phase = QT == 2 ? cnt & 1 : (cnt >> 1) & 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(s_full(sbuf), s_phase, abort_flag));
+                    ok = warp_wait(s_full(sbuf), s_phase, abort_flag);
                     if (!ok)
                         break;
                     if constexpr (kQuant) {
-                        // S is there, so the tile's scales are, and no later tile's yet: the wait
-                        // only orders the reads after the writes
-                        ok = __all_sync(0xffffffffu, mbar_wait(scale_full(tcnt & 1), (tcnt >> 1) & 1, abort_flag));
+                        ok = warp_wait(scale_full(tcnt % SCALES), (tcnt / SCALES) & 1, abort_flag);
                         if (!ok)
                             break;
                     }
                     tc_fence_after();
                     const uint32_t s_addr = lane_base + sbuf * BN;
-                    const float *scales = reinterpret_cast<const float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
+                    const uint32_t scales = sbase + lay.scales + ((tcnt % SCALES) * 3 * BN + col0) * 4;
                     if (warp_live) {
-                        uint32_t v[kCols];
-                        tmem_ld_row<kCols>(s_addr + col0, v);
-                        if constexpr (kQuant) {
-                            const uint64_t qs2 = f2(qscale, qscale);
-#pragma unroll
-                            for (int c = 0; c < kCols; c += 4) {
-                                const float4 ks = *reinterpret_cast<const float4 *>(scales + col0 + c);
-                                const float4 lv = *reinterpret_cast<const float4 *>(scales + BN + col0 + c);
-                                store2(v + c, fma2(mul2(load2(v + c), f2(ks.x, ks.y)), qs2, f2(lv.x, lv.y)));
-                                store2(v + c + 2, fma2(mul2(load2(v + c + 2), f2(ks.z, ks.w)), qs2, f2(lv.z, lv.w)));
-                            }
-                        }
+                        // An 8-bit cache's scores of 128 keys do not fit the registers beside everything
+                        // else: they are read from TMEM (and scaled) twice.
+                        constexpr bool kKeep = !kQuant || kCols <= 64;
+                        uint32_t v[kKeep ? kCols / 32 : 1][32];
                         const int rlo = lo - t0 - col0, rhi = hi - t0 - col0;
-                        if (__any_sync(0xffffffffu, rlo > 0 || rhi < kCols)) {
+                        const bool edge = __any_sync(0xffffffffu, rlo > 0 || rhi < kCols);
+                        // x_j of 32 keys from c0 (of this copy's), their S taken out of TMEM into x
+                        auto scores = [&](uint32_t(&x)[32], int c0) {
+                            tmem_ld_32x32b_x32(s_addr + col0 + c0, x);
+                            if constexpr (kQuant) {
+                                float4 ks[8], lv[8];
 #pragma unroll
-                            for (int c = 0; c < kCols; ++c)
-                                if (c < rlo || c >= rhi)
-                                    v[c] = 0xFF800000u;
-                        }
+                                for (int i = 0; i < 8; ++i)
+                                    ks[i] = lds4(scales + (c0 + 4 * i) * 4);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    lv[i] = lds4(scales + (BN + c0 + 4 * i) * 4);
+                                tmem_wait_ld(x);
+                                const uint64_t qs2 = f2(qscale, qscale);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    store2(x + 4 * i, fma2(mul2(load2(x + 4 * i), f2(ks[i].x, ks[i].y)), qs2,
+                                                           f2(lv[i].x, lv[i].y)));
+                                    store2(x + 4 * i + 2, fma2(mul2(load2(x + 4 * i + 2), f2(ks[i].z, ks[i].w)), qs2,
+                                                               f2(lv[i].z, lv[i].w)));
+                                }
+                            } else {
+                                tmem_wait_ld(x);
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    if (c0 + c < rlo || c0 + c >= rhi)
+                                        x[c] = 0xFF800000u;
+                            }
+                        };
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto raise = [&](const uint32_t(&x)[32]) {
 #pragma unroll
-                        for (int c = 0; c < kCols; c += 8)
+                            for (int c = 0; c < 32; c += 8)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                top[i] = fmaxf(top[i], fmaxf(__uint_as_float(v[c + 2 * i]), __uint_as_float(v[c + 2 * i + 1])));
+                                for (int i = 0; i < 4; ++i)
+                                    top[i] = fmaxf(top[i], fmaxf(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])));
+                        };
+                        if constexpr (kQuant) {
+#pragma unroll(kKeep ? 4 : 1)
+                            for (int i = 0; i < kCols / 32; ++i) {
+                                scores(v[kKeep ? i : 0], 32 * i);
+                                raise(v[kKeep ? i : 0]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kCols / 32; ++i)
+                                tmem_ld_32x32b_x32(s_addr + col0 + 32 * i, v[i]);
+#pragma unroll
+                            for (int i = 0; i < kCols / 32; ++i)
+                                tmem_wait_ld(v[i]);
+                            if (edge) {
+#pragma unroll
+                                for (int c = 0; c < kCols; ++c)
+                                    if (c < rlo || c >= rhi)
+                                        v[c / 32][c % 32] = 0xFF800000u;
+                            }
+#pragma unroll
+                            for (int i = 0; i < kCols / 32; ++i)
+                                raise(v[i]);
+                        }
                         const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
                         const bool move = live && rise > LAZY;
@@ -791,7 +995,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             tc_fence_after();
                             const float keep = move ? ex2(-rise) : 1.f;
                             l = kQuant && move ? l * ex2(-0.5f * rise) * ex2(-0.5f * rise) : l * keep;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < DP; c += 16) {
                                 uint32_t o[16];
                                 tmem_ld_32x32b_x16(lane_base + 256 + s * 128 + c, o);
@@ -817,12 +1021,21 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 if (2 * c < col0 || 2 * c >= col0 + kCols)
                                     tmem_st_32x32b_x16(s_addr + c, z);
                         }
-#pragma unroll
+#pragma unroll(kKeep ? 4 : 1)
                         for (int c0 = 0; c0 < kCols; c0 += 32) {
                             uint32_t p[16];
+                            float4 rv[8];
+                            if constexpr (kQuant) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    rv[i] = lds4(scales + (2 * BN + c0 + 4 * i) * 4);
+                            }
+                            if constexpr (!kKeep)  // P goes where S has been read already
+                                scores(v[0], c0);
+                            const uint32_t(&vc)[32] = v[kKeep ? c0 / 32 : 0];
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
-                                uint64_t x0 = load2(v + c0 + c), x1 = load2(v + c0 + c + 2);
+                                uint64_t x0 = load2(vc + c), x1 = load2(vc + c + 2);
                                 if constexpr (kQuant) {
                                     x0 = add2(x0, base2), x1 = add2(x1, base2);
                                 } else {
@@ -831,9 +1044,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 const float2 y0 = f2_split(x0), y1 = f2_split(x1);
                                 const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
                                 if constexpr (kQuant) {
-                                    const float4 rv = *reinterpret_cast<const float4 *>(scales + 2 * BN + col0 + c0 + c);
-                                    sum2[0] = fma2(f2(p0, p1), f2(rv.x, rv.y), sum2[0]);
-                                    sum2[1] = fma2(f2(p2, p3), f2(rv.z, rv.w), sum2[1]);
+                                    sum2[0] = fma2(f2(p0, p1), f2(rv[c / 4].x, rv[c / 4].y), sum2[0]);
+                                    sum2[1] = fma2(f2(p2, p3), f2(rv[c / 4].z, rv[c / 4].w), sum2[1]);
                                     p[c / 2] = f16_pack(p0, p1), p[c / 2 + 1] = f16_pack(p2, p3);
                                 } else {
                                     sum2[0] = add2(sum2[0], f2(p0, p1));
@@ -850,7 +1062,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     if constexpr (!kQuant) {
                         // rows of V that no row of the item sees may hold anything: 0 * NaN must not happen
                         if (s == 0 && (t0 < g.item.lo || t0 + BN > g.item.hi)) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(ring_full(vr.slot, 0), vr.phase, abort_flag));
+                            ok = warp_wait(ring_full(vr.slot, 0), vr.phase, abort_flag);
                             if (!ok)
                                 break;
                             if (t0 + row < g.item.lo || t0 + row >= g.item.hi) {
@@ -868,130 +1080,132 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0) {
                         mbar_arrive(p_full(sbuf));
+                        if (kQuant && s == 0)
+                            mbar_arrive(soft_done(tcnt & 1));
+                    }
                     ++cnt;
                     ++tcnt;
                 }
-            } else {
+            } else if (started) {
                 tcnt += g.tiles;
             }
             if (!ok)
                 break;
+            // the next item's queries go in while the last product of this one runs
+            const Segment &next = segs[(n + 1) & (SEGMENTS - 1)];
+            ok = seg_wait(n + 1);
+            if (!ok)
+                break;
+            more = next.tiles != 0;
+            if (more && active(next))
+                load_q(next);
+            if (!act) {
+                if (started)
+                    seg_done(n);
+                continue;
+            }
             const int tok = g.start + g.item.tok0 + s * a.tpm + rt;
             const int head = g.kvh * a.group + gi;
             const bool whole = g.first && g.last;
-            const int slot = 2 * cta + (g.u != cta * units / grid ? 1 : 0);
-            const long long part = static_cast<long long>(slot) * (QT * BM) + s * BM + trow;
+            const long long part = static_cast<long long>(g.slot) * (QT * BM) + s * BM + trow;
             uint16_t *dst = a.out.data + static_cast<long long>(tok) * a.out.token_stride +
                             static_cast<long long>(head) * a.out.head_stride;
-            if (lane == 0)
-                ww.have[which ^ 1] = ww.walk.next(a, ww.seg[which ^ 1]);
-            __syncwarp();
-            // the next item's queries go in while the last product of this one runs; with copies to
-            // add up their place is needed first
-            if (FOLD == 1 && ww.have[which ^ 1] && active(ww.seg[which ^ 1]))
-                load_q(ww.seg[which ^ 1]);
-            if (act) {
-                ok = __all_sync(0xffffffffu, mbar_wait(pv_done(s), (cnt - 1) & 1, abort_flag));
+            ok = warp_wait(pv_done(s), (cnt - 1) & 1, abort_flag);
+            if (!ok)
+                break;
+            tc_fence_after();
+            float weight = 1.f;
+            if constexpr (FOLD > 1) {
+                // the copies' common maximum; each copy's weight; the sum of their sums
+                float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold + BM * 32 * 4);
+                ml[row] = make_float2(m * sl2, l);
+                ok = fold_sync();
                 if (!ok)
                     break;
-                tc_fence_after();
-                float weight = 1.f;
-                if constexpr (FOLD > 1) {
-                    // the copies' common maximum; each copy's weight; the sum of their sums
-                    float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold);
-                    ml[row] = make_float2(m * sl2, l);
-                    ok = fold_sync();
-                    if (!ok)
-                        break;
-                    float top = -INFINITY;
+                float top = -INFINITY;
 #pragma unroll
-                    for (int f = 0; f < FOLD; ++f)
-                        top = fmaxf(top, ml[f * kRows + trow].x);
-                    const float b = top == -INFINITY ? 0.f : top;
-                    weight = exp2f(m * sl2 - b);
-                    l = 0.f;
+                for (int f = 0; f < FOLD; ++f)
+                    top = fmaxf(top, ml[f * kRows + trow].x);
+                const float b = top == -INFINITY ? 0.f : top;
+                weight = exp2f(m * sl2 - b);
+                l = 0.f;
 #pragma unroll
-                    for (int f = 0; f < FOLD; ++f) {
-                        const float2 x = ml[f * kRows + trow];
-                        // in one power, as in the combine kernel
-                        l += x.y > 0.f ? exp2f(x.x - b + log2f(x.y)) : x.y == 0.f ? 0.f : x.y;
-                    }
-                    m = top;
-                } else {
-                    m *= sl2;
+                for (int f = 0; f < FOLD; ++f) {
+                    const float2 x = ml[f * kRows + trow];
+                    // in one power, as in the combine kernel
+                    l += x.y > 0.f ? exp2f(x.x - b + log2f(x.y)) : x.y == 0.f ? 0.f : x.y;
                 }
-                const float inv = whole ? (l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l) : 1.f;
-                if (warp_live || FOLD > 1) {
-#pragma unroll
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
-                        tmem_wait_ld(o);
-                        constexpr int kPer = 32 / FOLD;  // elements of the 32 that this thread writes
-                        int k0 = 0;
-                        if constexpr (FOLD > 1) {
-                            // through shared memory (the queries' place, read by now): rows of 32 words,
-                            // word k of row r at k ^ (r mod 32)
-                            float *x = reinterpret_cast<float *>(smem + lay.q);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                x[row * 32 + (k ^ lane)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
-                            ok = ok && fold_sync();
-                            k0 = row / kRows * kPer;
-#pragma unroll
-                            for (int k = 0; k < kPer; ++k) {
-                                float sum = 0.f;
-#pragma unroll
-                                for (int f = 0; f < FOLD; ++f)
-                                    sum += x[(f * kRows + trow) * 32 + ((k0 + k) ^ lane)];
-                                o[k] = __float_as_uint(sum);
-                            }
-                            ok = ok && fold_sync();
-                        }
-                        if (live && whole) {
-#pragma unroll
-                            for (int k = 0; k < kPer; k += 8)
-                                if (c + k0 + k < dim)
-                                    *reinterpret_cast<uint4 *>(dst + c + k0 + k) = make_uint4(
-                                        bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
-                                        bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
-                                        bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
-                                        bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
-                        } else if (live) {
-#pragma unroll
-                            for (int k = 0; k < kPer; k += 4)
-                                if (c + k0 + k < dim)
-                                    *reinterpret_cast<uint4 *>(a.part_o + part * dim + c + k0 + k) =
-                                        make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                        }
-                    }
-                }
-                if (live && col0 == 0) {
-                    if (!whole)
-                        a.part_ml[part] = make_float2(m, l);
-                    else if (a.lse)
-                        a.lse[static_cast<long long>(tok) * a.q.heads + head] = (m + log2f(l)) * 0.69314718055994530942f;
-                }
-                if (s == 0 && row == 0 && g.first && !g.last) {
-                    const long long end = g.u + g.item.tiles - 1;  // the item's last unit
-                    SplitRecord rec;
-                    rec.valid = 1;
-                    rec.pad = 0;
-                    rec.first_slot = slot;
-                    rec.c0 = cta;
-                    rec.c1 = static_cast<int>(((end + 1) * grid - 1) / units);
-                    rec.kvh = g.kvh;
-                    rec.tok0 = g.start + g.item.tok0;
-                    rec.ntok = g.item.ntok;
-                    a.records[cta] = rec;
-                }
-                tc_fence_before();
+                m = top;
+            } else {
+                m *= sl2;
             }
-            if (FOLD > 1 && ok && ww.have[which ^ 1])
-                load_q(ww.seg[which ^ 1]);
-            __syncwarp();  // the other lanes are done with this segment before lane 0 writes over it
+            const float inv = whole ? (l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l) : 1.f;
+            if (warp_live || FOLD > 1) {
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
+                    tmem_wait_ld(o);
+                    constexpr int kPer = 32 / FOLD;  // elements of the 32 that this thread writes
+                    int k0 = 0;
+                    if constexpr (FOLD > 1) {
+                        // through shared memory: rows of 32 words, word k of row r at k ^ (r mod 32)
+                        float *x = reinterpret_cast<float *>(smem + lay.fold);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            x[row * 32 + (k ^ lane)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
+                        ok = ok && fold_sync();
+                        k0 = row / kRows * kPer;
+#pragma unroll
+                        for (int k = 0; k < kPer; ++k) {
+                            float sum = 0.f;
+#pragma unroll
+                            for (int f = 0; f < FOLD; ++f)
+                                sum += x[(f * kRows + trow) * 32 + ((k0 + k) ^ lane)];
+                            o[k] = __float_as_uint(sum);
+                        }
+                        ok = ok && fold_sync();
+                    }
+                    if (live && whole) {
+#pragma unroll
+                        for (int k = 0; k < kPer; k += 8)
+                            if (c + k0 + k < dim)
+                                *reinterpret_cast<uint4 *>(dst + c + k0 + k) = make_uint4(
+                                    bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
+                                    bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
+                                    bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
+                                    bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+                    } else if (live) {
+#pragma unroll
+                        for (int k = 0; k < kPer; k += 4)
+                            if (c + k0 + k < dim)
+                                *reinterpret_cast<uint4 *>(a.part_o + part * dim + c + k0 + k) =
+                                    make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                }
+            }
+            if (live && col0 == 0) {
+                if (!whole)
+                    a.part_ml[part] = make_float2(m, l);
+                else if (a.lse)
+                    a.lse[static_cast<long long>(tok) * a.q.heads + head] = (m + log2f(l)) * 0.69314718055994530942f;
+            }
+            if (s == 0 && row == 0 && g.first && !g.last) {
+                SplitRecord rec;
+                rec.valid = 1;
+                rec.pad = 0;
+                rec.first_slot = g.slot;
+                rec.c0 = cta;
+                rec.c1 = g.end_cta;
+                rec.kvh = g.kvh;
+                rec.tok0 = g.start + g.item.tok0;
+                rec.ntok = g.item.ntok;
+                a.records[cta] = rec;
+            }
+            tc_fence_before();
+            seg_done(n);
         }
     } else {
         // -------------------------------------------------------------------- 8-bit codes to f16
@@ -999,78 +1213,28 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             reg_dec<Shape<QT, TYPE>::kWideRegs>();
             const int kv = warp >= 8 + 4 * QT ? 1 : 0;
             const int t = threadIdx.x & 127;
-            const int ps = a.cache.page_size, dim = a.cache.dim;
+            const int dim = a.cache.dim;
             constexpr int kChunks = DP / 16;
-            Walk w;
-            w.begin(a, prefix, units, grid, cta);
-            Segment g;
-            int tcnt = 0;
-            // operand `item` (2 j for tile j's K, 2 j + 1 for its V) is in slot item mod size of a ring
-            int item = kv;
+            // operand 2 j is tile j's K, 2 j + 1 its V; operand i is in slot i mod size of a ring, for
+            // the (i / size)-th time
+            int rslot = kv, rround = 0, wslot = kv, wround = 0;
             bool ok = true;
-            while (ok && w.next(a, g)) {
-                const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
-                // this thread's key of a tile: its page, then (a tile later) its two scales
-                auto page_of = [&](int j) {
-                    const int tok = (g.tile + j) * BN + t;
-                    return j < g.tiles && tok >= g.item.lo && tok < g.item.hi ? __ldg(pt + tok / ps) : -1;
-                };
-                auto scales_of = [&](int j, int page) {
-                    const int tok = (g.tile + j) * BN + t;
-                    float2 r = make_float2(0.f, -1.f);  // no key there
-                    if (j < g.tiles && tok >= g.item.lo && tok < g.item.hi) {
-                        page = min(max(page, 0), a.cache.pages - 1);
-                        const long long at = (static_cast<long long>(page) * a.cache.heads + g.kvh) * ps + tok % ps;
-                        r = make_float2(__ldg(a.cache.k_scale + at), __ldg(a.cache.v_scale + at));
-                    }
-                    return r;
-                };
-                float2 sc = kv == 0 ? scales_of(0, page_of(0)) : make_float2(0.f, 0.f);
-                int page = kv == 0 ? page_of(1) : 0;
-                float top_lv = -INFINITY;  // this thread's largest log2 of a value scale in the segment
-                for (int j = 0; j < g.tiles && ok; ++j) {
-                    const int t0 = (g.tile + j) * BN;
-                    float2 next_sc = sc;
-                    if (kv == 0) {
-                        next_sc = scales_of(j + 1, page);
-                        page = page_of(j + 2);
-                    }
-                    const int wslot = item % WIDE_RING, rslot = item % a.ring;
+            for (int n = 0; ok; ++n) {
+                ok = seg_wait(n);
+                if (!ok || segs[n % SEGMENTS].tiles == 0)
+                    break;
+                const Segment &g = segs[n % SEGMENTS];
+                const int tiles = g.tiles, first = g.tile * BN, item_lo = g.item.lo, item_hi = g.item.hi;
+                for (int j = 0; j < tiles && ok; ++j) {
+                    const int t0 = first + j * BN;
                     // the n-th time (from 0) that this warpgroup takes over the slot, -1: it was free
-                    const int turn = item / (2 * WIDE_RING) - (kv == 0 ? wslot != 1 : wslot == 1);
+                    const int turn = kWide % 2 == 0 ? wround - 1 : (wround >> 1) - (kv == 0 ? wslot != 1 : wslot == 1);
                     if (turn >= 0)
-                        ok = __all_sync(0xffffffffu, mbar_wait(wide_empty(wslot, kv), turn & 1, abort_flag));
+                        ok = warp_wait(wide_empty(wslot, kv), turn & 1, abort_flag);
                     if (!ok)
                         break;
-                    if (kv == 0) {
-                        // the slot's last reader, the softmax two tiles back, is done: this wide
-                        // slot held that tile's V or a later operand
-                        float *sm = reinterpret_cast<float *>(smem + lay.scales) + (tcnt & 1) * 3 * BN;
-                        float lv = sc.y > 0.f ? __log2f(sc.y) : sc.y == 0.f ? -INFINITY : sc.y;
-                        float rv = sc.y != 0.f ? __frcp_rn(sc.y) : 0.f;
-                        if (sc.y > 0.f)
-                            top_lv = fmaxf(top_lv, lv);
-                        if (__any_sync(0xffffffffu, sc.y == 0.f)) {
-                            // A row of zeros adds to l alone; any scale serves its codes.  One 2^60
-                            // below the largest seen keeps it from setting m' (P' of the others would
-                            // fall out of f16) and its own P' far above float32's least.
-                            float ref = top_lv;
-                            for (int o = 16; o > 0; o >>= 1)
-                                ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-                            if (sc.y == 0.f) {
-                                lv = fmaxf(floorf(ref) - 60.f, kLeastScale);
-                                rv = exp2f(-lv);
-                            }
-                        }
-                        sm[t] = sc.x;
-                        sm[BN + t] = lv;
-                        sm[2 * BN + t] = rv;
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(scale_full(tcnt & 1));
-                    }
-                    const uint32_t r_phase = (item / a.ring) >> (a.ring & 1) & 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(ring_full(rslot, kv), r_phase, abort_flag));
+                    const uint32_t r_phase = rround >> (a.ring & 1) & 1;
+                    ok = warp_wait(ring_full(rslot, kv), r_phase, abort_flag);
                     if (!ok)
                         break;
                     const uint8_t *src = smem + lay.ring + rslot * lay.ring_stage;
@@ -1083,11 +1247,11 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         v[i] = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
                     }
                     const int c = t % kChunks, odd = c >> 2, c0 = 2 * (c & 3);
-                    if (t0 < g.item.lo || t0 + BN > g.item.hi || c * 16 >= dim) {
+                    if (t0 < item_lo || t0 + BN > item_hi || c * 16 >= dim) {
 #pragma unroll
                         for (int i = 0; i < kChunks; ++i) {
                             const int r = i * (128 / kChunks) + t / kChunks;
-                            if (t0 + r < g.item.lo || t0 + r >= g.item.hi || c * 16 >= dim)
+                            if (t0 + r < item_lo || t0 + r >= item_hi || c * 16 >= dim)
                                 v[i] = make_uint4(0, 0, 0, 0);
                         }
                     }
@@ -1110,10 +1274,18 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         mbar_arrive(ring_empty(rslot));
                         mbar_arrive(wide_full(wslot));
                     }
-                    item += 2;
-                    sc = next_sc;
-                    ++tcnt;
+                    rslot += 2;
+                    if (rslot >= a.ring) {
+                        rslot -= a.ring;
+                        ++rround;
+                    }
+                    wslot += 2;
+                    if (wslot >= kWide) {
+                        wslot -= kWide;
+                        ++wround;
+                    }
                 }
+                seg_done(n);
             }
         }
     }
@@ -1248,9 +1420,9 @@ template <int DP, int QT, int TYPE, int FOLD>
 cudaError_t launch(Args a, int sms, cudaStream_t stream)
 {
     a.ring = MAX_RING;
-    while (a.ring > 3 && layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024 > SMEM_LIMIT)
+    while (a.ring > 3 && layout_of<DP, QT, TYPE, FOLD>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024 > SMEM_LIMIT)
         --a.ring;
-    const int smem = layout_of<DP, QT, TYPE>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024;
+    const int smem = layout_of<DP, QT, TYPE, FOLD>(a.ring, a.cache.dim, a.tokens.B).bytes + 1024;
     if (smem > SMEM_LIMIT)
         return cudaErrorInvalidConfiguration;
     CUtensorMap mk, mv;
@@ -1317,6 +1489,12 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     a.tpm = BM / fold / a.group;
     a.span = tiles * a.tpm;
     a.box = std::gcd(cache.page_size, BN);
+    // ceil(2^(31 + b) / page_size) with b = ceil(log2(page_size)) gives the exact quotient below 2^31
+    int bits = 3;
+    while ((1 << bits) < cache.page_size)
+        ++bits;
+    a.page_magic = static_cast<uint32_t>(((1ull << (31 + bits)) + cache.page_size - 1) / cache.page_size);
+    a.page_shift = static_cast<uint32_t>(bits - 1);
     a.status = status;
     const Scratch s = scratch_of(sms, tiles, cache.dim);
     uint8_t *p = static_cast<uint8_t *>(scratch);

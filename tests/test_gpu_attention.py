@@ -429,6 +429,24 @@ def test_attention_repeats_its_bits(at):
         assert torch.equal(got["out"], ref["out"]) and torch.equal(got["lse"], ref["lse"])
 
 
+@TYPES
+@pytest.mark.parametrize("new", [2, 40])
+def test_attention_long(at, dtype, new):
+    """So many key tiles for each SM that every ring wraps many times over, and no wait gives up."""
+    from speculative_decoding_drafter_gb300 import dflash2 as df
+
+    n, kvh, dim = 163000, 8, 64
+    b = Batch([n], [new], 64, poison=True)
+    cache, k, v = filled(at, b, kvh, dim, dtype, 5)
+    q = randn(gen(6), new, 16, dim).to(BF16)
+    ws = at.AttentionWorkspace(cache, b.on_gpu(at), 16)
+    want, mag, lse = attend(q, k, v, b.lens, b.news, dim ** -0.5, True, 0)
+    got = at.dflash2_paged_attention(q, cache, b.on_gpu(at), workspace=ws)
+    df.dflash2_check_device_status(ws)
+    assert ((got["out"].double() - want).abs() <= attend_bound(want, mag)).all()
+    assert ((got["lse"].double() - lse).abs() <= 2.0 ** -14 * (1 + lse.abs())).all()
+
+
 def test_attention_many_sequences(at):
     """More sequences than lanes, SMs and probes of one lookup step, several of them empty."""
     lens = [(37 * i) % 211 for i in range(600)]
