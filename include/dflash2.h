@@ -347,9 +347,8 @@ DF2_API df2_status dflash2_rope(const df2_rope *rope, int32_t N, int32_t dim, co
 
 typedef enum df2_cache_type { DF2_CACHE_BF16 = 0, DF2_CACHE_E4M3 = 1, DF2_CACHE_INT8 = 2 } df2_cache_type;
 
-/* One layer's paged cache: k and v [pages, heads, page_size, dim] of the type (16-byte
- * aligned), and for the 8-bit types k_scale and v_scale float [pages, heads, page_size] (4-byte
- * aligned; NULL for bf16).  A row (one token, one head) is held as codes times its scale:
+/* One layer's paged cache: k and v [pages, heads, page_size, dim] of the type, and for the 8-bit
+ * types k_scale and v_scale float [pages, heads, page_size] (NULL for bf16), all 16-byte aligned.  A row (one token, one head) is held as codes times its scale:
  *   m = max |row|,  scale = m / M,  code = round(row * (M / m)),  M = 448 (e4m3) or 127 (int8),
  * each operation in float32, codes rounded to nearest even.  A row with m < 1e-30 is held as
  * zeros; one that is not finite gets a NaN scale and reads back as NaN throughout.
@@ -366,7 +365,7 @@ typedef struct df2_cache {
  * lives in page page_table[b, position / page_size].  All three are device arrays.
  *   token_start int32 [B + 1], rising from 0 to N;  kv_len int32 [B];
  *   page_table int32 [B, max_pages]: only the entries of positions that a call touches are used.
- * max_new: no n_b is larger.  B <= 2048.  A row whose position is negative (kv_len[b] < n_b) is padding: it
+ * max_new: no n_b is larger.  B <= 2048, max_pages * page_size <= 2^30.  A row whose position is negative (kv_len[b] < n_b) is padding: it
  * is not written, reads back as zeros, and with causal attention sees nothing.  Page ids outside
  * [0, pages) and positions past max_pages * page_size are the caller's mistake: they are not
  * written, read back as zeros and are attended to with unspecified results, but no access

@@ -78,7 +78,7 @@ df2_status check_cache(const df2_cache *c)
     if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
         return DF2_ERR_INVALID_ARG;
     if (c->type != DF2_CACHE_BF16 &&
-        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+        (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)))
         return DF2_ERR_INVALID_ARG;
     return DF2_OK;
 }
@@ -99,7 +99,7 @@ df2_status check_tokens(const df2_tokens *t, int page_size)
     if (!t->token_start || !t->kv_len || !aligned(t->token_start, 4) || !aligned(t->kv_len, 4) ||
         (t->max_pages > 0 && (!t->page_table || !aligned(t->page_table, 4))))
         return DF2_ERR_INVALID_ARG;
-    if (static_cast<long long>(t->max_pages) * page_size >= (1LL << 31) - 1024)
+    if (static_cast<long long>(t->max_pages) * page_size > (1LL << 30))
         return DF2_ERR_UNSUPPORTED;
     return DF2_OK;
 }

@@ -46,10 +46,10 @@ constexpr int BM = 128;  // rows of a tile
 constexpr int BN = 128;  // keys of a tile
 constexpr int HALF_BYTES = 128 * 128;  // 128 rows of 64 16-bit elements
 constexpr int SMEM_LIMIT = 227 * 1024;
-constexpr int MAX_RING = 8;
+constexpr int MAX_RING = 12;
 constexpr int MAX_WIDE = 4;
 constexpr int SEGMENTS = 4;  // segments that the walking warp may be ahead
-constexpr int SCALES = 4;  // tiles whose scales are held
+constexpr int MAX_SCALES = 4;
 constexpr float kLeastScale = -108.f;  // log2 of the least scale a cache holds, 1e-30 / 448
 constexpr float LAZY = 8.f;   // how far the running maximum may lag, in powers of two
 
@@ -86,13 +86,20 @@ __device__ __forceinline__ int page_of_token(const Args &a, int token)
     return static_cast<int>(__umulhi(static_cast<uint32_t>(token), a.page_magic) >> a.page_shift);
 }
 
-__device__ __forceinline__ Sequence sequence_at(const Args &a, int b)
+constexpr int NEAR = 32;  // sequences whose numbers a CTA keeps in shared memory
+
+__device__ __forceinline__ Sequence load_sequence(const Args &a, int b)
 {
     Sequence s;
     s.start = min(max(__ldg(a.tokens.token_start + b), 0), a.tokens.N);
     s.n = min(max(__ldg(a.tokens.token_start + b + 1), s.start), a.tokens.N) - s.start;
     s.len = min(max(__ldg(a.tokens.kv_len + b), 0), a.tokens.max_pages * a.cache.page_size);
     return s;
+}
+
+__device__ __forceinline__ Sequence sequence_at(const Args &a, const Sequence *near, int b)
+{
+    return b < NEAR ? near[b] : load_sequence(a, b);
 }
 
 struct Item {
@@ -139,9 +146,11 @@ struct Walk {
     long long u, u_begin, u_end;
     int b, kvh, qt, off, nq;
     Sequence s;
+    const Sequence *near;
 
-    __device__ __forceinline__ void begin(const Args &a, const int *prefix, long long units, int grid, int c)
+    __device__ __forceinline__ void begin(const Args &a, const Sequence *near_, const int *prefix, long long units, int grid, int c)
     {
+        near = near_;
         u = u_begin = c * units / grid;
         u_end = (c + 1) * units / grid;
         int lo = 0, hi = a.tokens.B;  // the largest b with prefix[b] * heads <= u
@@ -153,7 +162,7 @@ struct Walk {
                 hi = mid;
         }
         b = lo;
-        s = sequence_at(a, b);
+        s = sequence_at(a, near, b);
         nq = items_of(a, s);
         const int per_head = max(prefix[b + 1] - prefix[b], 1);
         const int r = static_cast<int>(u - static_cast<long long>(prefix[b]) * a.cache.heads);
@@ -175,7 +184,7 @@ struct Walk {
         }
         while (kvh == a.cache.heads) {  // the next sequence that has tokens
             ++b;
-            s = sequence_at(a, b);
+            s = sequence_at(a, near, b);
             nq = items_of(a, s);
             kvh = nq > 0 ? 0 : a.cache.heads;
         }
@@ -199,6 +208,26 @@ struct Walk {
             }
         }
         return true;
+    }
+};
+
+// Where one kind of operand is in a ring that both share: operand 2 j is tile j's K, 2 j + 1 its V,
+// operand i is in slot i mod size, for the (i / size)-th time.
+struct RingSlot {
+    int slot, round;
+    __device__ __forceinline__ void step(int size)
+    {
+        slot += 2;
+        if (slot >= size) {
+            slot -= size;
+            ++round;
+        }
+    }
+    // The n-th time (from 0) that this kind takes the slot over from its last user; -1: it was free.
+    // In a ring of odd size a slot holds the two kinds in turn.
+    __device__ __forceinline__ int turn(int size, int kv) const
+    {
+        return (size & 1) == 0 ? round - 1 : (round >> 1) - ((slot & 1) == kv ? 1 : 0);
     }
 };
 
@@ -252,6 +281,8 @@ template <int QT, int TYPE>
 struct Shape {
     // widened tiles: two K and two V; with two row tiles there is room for three in rotation
     static constexpr int kWideRing = QT == 1 ? 4 : 3;
+    // tiles whose scales are held, ready (see soft_done) and as they lie
+    static constexpr int kScales = QT == 1 ? 2 : 4, kRaws = QT == 1 ? 4 : 2;
     static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 2 : 0));
     // registers of a thread after the roles part: control, softmax, widening (their sum times 128
     // is at most what the launch holds: 65536 / threads, a multiple of 8, times the threads)
@@ -265,12 +296,12 @@ struct Shape {
 };
 
 // Shared memory: Q tiles (two row tiles; one tile's queries are in TMEM) | TMA ring | widened ring
-// (8-bit) | scales (8-bit) | place to add copies up, their (m, l) | barriers | segments | prefix sums.
+// (8-bit) | scales, and as they lie (8-bit) | place to add copies up, their (m, l) | barriers | segments | sequences | prefix sums.
 struct Layout {
-    int q, ring, ring_stage, wide, scales, fold, bars, segs, prefix, bytes;
+    int q, ring, ring_stage, wide, scales, raw, fold, bars, segs, near, prefix, bytes;
 };
 
-constexpr int BAR_COUNT = 3 * MAX_RING + 3 * MAX_WIDE + 2 + 2 + 2 + 2 + SCALES + 1 + 1 + 2 + 2 * SEGMENTS;  // tmem slot and abort flag follow
+constexpr int BAR_COUNT = 4 * MAX_RING + 3 * MAX_WIDE + 2 + 2 + 2 + 2 + 3 * MAX_SCALES + 1 + 1 + 2 + 2 * SEGMENTS;  // tmem slot and abort flag follow
 
 template <int DP, int QT, int TYPE, int FOLD>
 __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
@@ -282,10 +313,12 @@ __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
     l.ring_stage = TYPE ? 128 * dim : tile;
     l.wide = l.ring + ring * l.ring_stage;
     l.scales = l.wide + (TYPE ? Shape<QT, TYPE>::kWideRing * tile : 0);
-    l.fold = l.scales + (TYPE ? SCALES * 3 * BN * 4 : 0);
-    l.bars = l.fold + (FOLD > 1 ? BM * 32 * 4 + BM * 8 : 0);
+    l.raw = l.scales + (TYPE ? Shape<QT, TYPE>::kScales * 3 * BN * 4 : 0);
+    l.fold = l.raw + (TYPE ? Shape<QT, TYPE>::kRaws * 2 * BN * 4 : 0);
+    l.bars = l.fold + (FOLD > 1 ? BM * 16 * 4 + BM * 8 : 0);
     l.segs = l.bars + BAR_COUNT * 8 + 8;
-    l.prefix = l.segs + SEGMENTS * static_cast<int>(sizeof(Segment));
+    l.near = l.segs + SEGMENTS * static_cast<int>(sizeof(Segment));
+    l.prefix = l.near + NEAR * static_cast<int>(sizeof(Sequence));
     l.bytes = l.prefix + (B + 1) * 4;
     return l;
 }
@@ -316,15 +349,22 @@ __device__ __forceinline__ void store2(uint32_t *v, uint64_t x)
     v[1] = __float_as_uint(f.y);
 }
 
-__device__ __forceinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort_flag)
-{
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
-}
+// A converged warp's wait for the phase of parity `parity`; false when another role gave up, or
+// after kWaitCycles, when it gives up itself.  (As short as it can be: it is inlined everywhere.)
+constexpr long long kWaitCycles = 2000000000;  // about a second
 
-// A converged warp's wait; what has to poll does so out of line.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
 {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    const long long t0 = clock64();
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || clock64() - t0 > kWaitCycles)) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 template <int N>
@@ -348,6 +388,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     constexpr int kTile = kHalves * HALF_BYTES;
     constexpr bool kQuant = TYPE != 0;
     constexpr int kWide = Shape<QT, TYPE>::kWideRing;
+    constexpr int kScales = Shape<QT, TYPE>::kScales, kRaws = Shape<QT, TYPE>::kRaws;
     constexpr int kRows = BM / FOLD;  // distinct rows of a tile
     constexpr int kCols = BN / FOLD;  // keys of a tile that a thread takes
     constexpr int kQCol = 384;        // TMEM: two S at 0 and 128, O at 256 (and 384), one tile's Q at 384
@@ -359,31 +400,34 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bar0 = sbase + lay.bars;
     // A barrier's phases are told apart by parity, so whoever waits on one must wait for every phase
-    // of it.  The slots of the odd-sized widened ring (and of the TMA ring, if its size is odd) hold
-    // a K and a V in turn, which different warpgroups widen: each has barriers of its own.
+    // of it.  The slots of a ring of odd size hold a K and a V in turn, which different warps load and
+    // widen: each has barriers of its own (next_kv: what the slot becomes free for).
     auto ring_full = [&](int s, int kv) { return bar0 + 8u * (s + (kQuant ? kv * MAX_RING : 0)); };
-    auto ring_empty = [&](int s) { return bar0 + 8u * (2 * MAX_RING + s); };
-    auto wide_full = [&](int s) { return bar0 + 8u * (3 * MAX_RING + s); };
-    auto wide_empty = [&](int s, int next_kv) { return bar0 + 8u * (3 * MAX_RING + MAX_WIDE * (1 + next_kv) + s); };
-    constexpr int kRest = 3 * MAX_RING + 3 * MAX_WIDE;
+    auto ring_empty = [&](int s, int next_kv) { return bar0 + 8u * (MAX_RING * (2 + next_kv) + s); };
+    auto wide_full = [&](int s) { return bar0 + 8u * (4 * MAX_RING + s); };
+    auto wide_empty = [&](int s, int next_kv) { return bar0 + 8u * (4 * MAX_RING + MAX_WIDE * (1 + next_kv) + s); };
+    constexpr int kRest = 4 * MAX_RING + 3 * MAX_WIDE;
     auto s_full = [&](int x) { return bar0 + 8u * (kRest + x); };
     auto p_full = [&](int x) { return bar0 + 8u * (kRest + 2 + x); };
     auto pv_done = [&](int s) { return bar0 + 8u * (kRest + 4 + s); };
     auto q_full = [&](int s) { return bar0 + 8u * (kRest + 6 + s); };
     auto scale_full = [&](int s) { return bar0 + 8u * (kRest + 8 + s); };
-    const uint32_t drain_bar = bar0 + 8u * (kRest + 8 + SCALES);
-    const uint32_t fold_bar = bar0 + 8u * (kRest + 9 + SCALES);
-    auto soft_done = [&](int x) { return bar0 + 8u * (kRest + 10 + SCALES + x); };
-    auto seg_full = [&](int i) { return bar0 + 8u * (kRest + 12 + SCALES + i); };
-    auto seg_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + SCALES + SEGMENTS + i); };
+    const uint32_t drain_bar = bar0 + 8u * (kRest + 8 + MAX_SCALES);
+    const uint32_t fold_bar = bar0 + 8u * (kRest + 9 + MAX_SCALES);
+    auto soft_done = [&](int x) { return bar0 + 8u * (kRest + 10 + MAX_SCALES + x); };
+    auto seg_full = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + i); };
+    auto seg_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + SEGMENTS + i); };
+    auto raw_full = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + 2 * SEGMENTS + i); };
+    auto raw_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + 2 * MAX_SCALES + 2 * SEGMENTS + i); };
     // what the MMAs read: the TMA ring itself, or the widened one
     const int op_size = kQuant ? kWide : a.ring;
     const uint32_t op_base = sbase + (kQuant ? lay.wide : lay.ring);
     auto op_full = [&](int s) { return kQuant ? wide_full(s) : ring_full(s, 0); };
-    auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, kWide % 2 ? 1 - kv : kv) : ring_empty(s); };
+    auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, kWide & 1 ? 1 - kv : kv) : ring_empty(s, a.ring & 1 ? 1 - kv : kv); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.bars + BAR_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
+    Sequence *near = reinterpret_cast<Sequence *>(smem + lay.near);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -392,7 +436,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_init(ring_full(s, 0), 1);
             if (kQuant)
                 mbar_init(ring_full(s, 1), 1);
-            mbar_init(ring_empty(s), kQuant ? 4 : 1);
+            mbar_init(ring_empty(s, 0), kQuant ? 4 : 1);
+            mbar_init(ring_empty(s, 1), kQuant ? 4 : 1);
         }
         for (int s = 0; s < kWide; ++s) {
             mbar_init(wide_full(s), 4);
@@ -406,11 +451,16 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_init(q_full(s), 4);
             mbar_init(soft_done(s), 4);
         }
-        for (int s = 0; s < SCALES; ++s)
+        for (int s = 0; s < kScales; ++s) {
             mbar_init(scale_full(s), 1);
+        }
+        for (int s = 0; s < kRaws; ++s) {
+            mbar_init(raw_full(s), 2);
+            mbar_init(raw_empty(s), 1);
+        }
         for (int s = 0; s < SEGMENTS; ++s) {
             mbar_init(seg_full(s), 1);
-            mbar_init(seg_empty(s), 1 + 4 * QT + (kQuant ? 2 + 8 : 0));  // warps that read it
+            mbar_init(seg_empty(s), 2 + 4 * QT + (kQuant ? 1 + 8 : 0));  // warps that read it
         }
         mbar_init(drain_bar, 1);
         mbar_init(fold_bar, 4);
@@ -429,7 +479,9 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const int B = a.tokens.B;
     if (B <= kThreads / 32) {
         if (warp < B) {
-            const Sequence s = sequence_at(a, warp);
+            const Sequence s = load_sequence(a, warp);
+            if (lane == 0)
+                near[warp] = s;
             const int nq = items_of(a, s);
             int t = 0;
             for (int qt = lane; qt < nq; qt += 32)
@@ -441,7 +493,9 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         }
     } else {
         for (int b = threadIdx.x; b < B; b += kThreads) {
-            const Sequence s = sequence_at(a, b);
+            const Sequence s = load_sequence(a, b);
+            if (b < NEAR)
+                near[b] = s;
             const int nq = items_of(a, s);
             int t = 0;
             for (int qt = 0; qt < nq; ++qt)
@@ -486,79 +540,133 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     if (!works) {
         if (threadIdx.x == 0)
             a.records[cta].valid = 0;
-    } else if (warp == 0) {
-        // ---------------------------------------------------------------- TMA producer
+    } else if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------------------- TMA producers: K, V
+        // Warp 0 also walks.  One lane issues with warp-uniform operands, box after box: lanes that
+        // issue their own boxes are taken one by one anyhow, at several times the cost.
         if constexpr (Shape<QT, TYPE>::kSplitRegs)
             reg_dec<Shape<QT, TYPE>::kControlRegs>();
+        const int kv = warp == 0 ? 0 : 1;
+        const CUtensorMap *map = kv ? &map_v : &map_k;
+        const float *scale_base = kv ? a.cache.v_scale : a.cache.k_scale;
         Walk walk;
-        walk.begin(a, prefix, units, grid, cta);
-        Segment g;
-        const int boxes = BN / a.box;
+        if (kv == 0)
+            walk.begin(a, near, prefix, units, grid, cta);
+        const int boxes = BN / a.box, per_batch = 32 / boxes;  // boxes of a tile, tiles of a batch of 32
         const int ps = a.cache.page_size, dim = a.cache.dim;
         const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
-        int slot = 0;
-        uint32_t phase = 0;
-        long long issued = 0;
+        RingSlot rs{kv, 0};
+        int tcnt = 0;  // tiles begun
         bool ok = true;
         for (int n = 0; ok; ++n) {
-            if (n >= SEGMENTS)
-                ok = warp_wait(seg_empty(n % SEGMENTS), (n / SEGMENTS - 1) & 1, abort_flag);
-            if (!ok)
-                break;
-            const bool have = walk.next(a, cta, units, grid, g);
-            if (lane == 0) {
-                segs[n % SEGMENTS] = g;
-                mbar_arrive(seg_full(n % SEGMENTS));
+            const Segment &g = segs[n % SEGMENTS];
+            if (kv == 0) {
+                if (n >= SEGMENTS)
+                    ok = warp_wait(seg_empty(n % SEGMENTS), (n / SEGMENTS - 1) & 1, abort_flag);
+                if (!ok)
+                    break;
+                Segment next;
+                walk.next(a, cta, units, grid, next);
+                if (lane == 0) {
+                    segs[n % SEGMENTS] = next;
+                    mbar_arrive(seg_full(n % SEGMENTS));
+                }
+                __syncwarp();
+            } else {
+                ok = seg_wait(n);
             }
-            __syncwarp();
-            if (!have)
+            const int tiles = g.tiles, kvh = g.kvh;
+            if (!ok || tiles == 0)
                 break;
             const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
-            auto page_of = [&](int tile) {
-                const int tok = tile * BN + lane * a.box;
-                const bool need = lane < boxes && tok < g.item.hi && tok + a.box > g.item.lo;
+            const int tok0 = g.tile * BN, lo = g.item.lo, hi = g.item.hi;
+            // 32 boxes' pages at a time, a lane each, the next 32 on their way: a load waits hundreds of
+            // cycles, too long to be met at every tile
+            auto pages_at = [&](int j) {
+                const int tok = tok0 + j * BN + lane * a.box;
+                const bool need = tok < hi && tok + a.box > lo;
                 return need ? min(max(__ldg(pt + page_of_token(a, tok)), 0), a.cache.pages - 1) : -1;
             };
-            int page = page_of(g.tile);
-            for (int j = 0; j < g.tiles && ok; ++j) {
-                const int tok = (g.tile + j) * BN + lane * a.box;
-                const int next_page = j + 1 < g.tiles ? page_of(g.tile + j + 1) : -1;
-                const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * box_bytes;
+            int batch = pages_at(0), next_batch = pages_at(per_batch), at = 0;
+            uint32_t needed = __ballot_sync(0xffffffffu, batch >= 0);
+            for (int j = 0; j < tiles; ++j) {
+                if (at == 32) {
+                    at = 0;
+                    batch = next_batch;
+                    needed = __ballot_sync(0xffffffffu, batch >= 0);
+                    next_batch = pages_at(j + per_batch);
+                }
+                const int tok = tok0 + j * BN;
+                const int here = __popc(needed >> at & ((1u << boxes) - 1u));
+                const int rw = tcnt % kRaws;
+                if constexpr (kQuant) {
+                    if (tcnt >= kRaws)
+                        ok = warp_wait(raw_empty(rw), (tcnt / kRaws - 1) & 1, abort_flag);
+                }
+                const int turn = rs.turn(a.ring, kv);
+                if (ok && turn >= 0)
+                    ok = warp_wait(ring_empty(rs.slot, kv), turn & 1, abort_flag);
+                if (!ok)
+                    break;
+                const uint32_t full = ring_full(rs.slot, kv);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full, here * box_bytes);
+                    if constexpr (kQuant)
+                        mbar_arrive_expect_tx(raw_full(rw), here * a.box * 4);
+                }
+                __syncwarp();
+                uint32_t dst = sbase + lay.ring + rs.slot * lay.ring_stage;
+                uint32_t raw_dst = sbase + lay.raw + (rw * 2 + kv) * BN * 4;
+                int in_page = tok - page_of_token(a, tok) * ps;
+#pragma unroll 1
+                for (int i = 0; i < boxes; i += 4) {
+                    int page[4], x[4];
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    ok = warp_wait(ring_empty(slot), phase ^ 1u, abort_flag);
-                    if (!ok)
-                        break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(ring_full(slot, kv), bytes);
-                    __syncwarp();
-                    if (page >= 0) {
-                        const int in_page = tok - page_of_token(a, tok) * ps;
-                        const CUtensorMap *map = kv ? &map_v : &map_k;
-                        const uint32_t dst = sbase + lay.ring + slot * lay.ring_stage;
-                        if constexpr (kQuant) {
-                            tma_load_4d(dst + lane * a.box * dim, map, ring_full(slot, kv), 0, in_page, g.kvh, page);
-                        } else {
+                    for (int k = 0; k < 4; ++k) {
+                        page[k] = __shfl_sync(0xffffffffu, batch, (at + i + k) & 31);
+                        page[k] = i + k < boxes ? page[k] : -1;
+                        x[k] = in_page;
+                        in_page += a.box;
+                        in_page = in_page == ps ? 0 : in_page;
+                    }
+                    if (elect_one()) {
 #pragma unroll
-                            for (int h = 0; h < kHalves; ++h)
-                                tma_load_4d(dst + h * HALF_BYTES + lane * a.box * 128, map, ring_full(slot, kv), h * 64,
-                                            in_page, g.kvh, page);
+                        for (int k = 0; k < 4; ++k) {
+                            if (page[k] >= 0) {
+                                const uint32_t to = dst + k * a.box * (kQuant ? dim : 128);
+                                if constexpr (kQuant) {
+                                    tma_load_4d(to, map, full, 0, x[k], kvh, page[k]);
+                                    bulk_load(raw_dst + k * a.box * 4,
+                                              scale_base + (static_cast<long long>(page[k]) * a.cache.heads + kvh) * ps + x[k],
+                                              a.box * 4, raw_full(rw));
+                                } else {
+#pragma unroll
+                                    for (int h = 0; h < kHalves; ++h)
+                                        tma_load_4d(to + h * HALF_BYTES, map, full, h * 64, x[k], kvh, page[k]);
+                                }
+                            }
                         }
                     }
                     __syncwarp();
-                    ++issued;
-                    if (++slot == a.ring) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
+                    dst += 4 * a.box * (kQuant ? dim : 128);
+                    raw_dst += 4 * a.box * 4;
                 }
-                page = next_page;
+                at += boxes;
+                rs.step(a.ring);
+                ++tcnt;
             }
+            if (ok && kv == 1)
+                seg_done(n);
         }
         if (!ok) {  // let the copies already issued land before the CTA leaves
-            for (long long n = issued > a.ring ? issued - a.ring : 0; n < issued; ++n)
-                drain_wait(ring_full(static_cast<int>(n % a.ring), static_cast<int>(n & 1)),
-                           static_cast<uint32_t>((n / a.ring) >> (kQuant && (a.ring & 1) ? 1 : 0)) & 1u);
+            for (int n = max(tcnt - a.ring, 0); n < tcnt; ++n) {
+                const int i = 2 * n + kv, round = i / a.ring;
+                drain_wait(ring_full(i % a.ring, kv), (kQuant && (a.ring & 1) ? round >> 1 : round) & 1);
+            }
+            if constexpr (kQuant) {
+                for (int n = max(tcnt - kRaws, 0); n < tcnt; ++n)
+                    drain_wait(raw_full(n % kRaws), (n / kRaws) & 1);
+            }
         }
     } else if (warp < 4) {
         if constexpr (Shape<QT, TYPE>::kSplitRegs)
@@ -624,68 +732,71 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 const int tiles = g.tiles;
                 if (tiles == 0)
                     break;
+                // one call site each for the two products, again for the instruction cache
                 if constexpr (QT == 2) {
+                    // PV of a row tile, then its next S: while one tile's softmax runs, the other's
+                    // products do
                     const int mt = g.item.ntok > a.tpm ? 2 : 1;
-                    for (int s = 0; s < mt; ++s) {
-                        DF2_WAIT(q_full(s), q_phase[s]);
-                        q_phase[s] ^= 1u;
-                    }
-                    if (!ok)
-                        break;
-                    DF2_WAIT(op_full(kr.slot), kr.phase);
-                    tc_fence_after();
-                    for (int s = 0; s < mt; ++s)
-                        qk(s, s, kr.slot);
-                    commit(op_empty(kr.slot, 0));
-                    kr.step(op_size);
-                    for (int j = 0; j < tiles && ok; ++j) {
+#pragma unroll 1
+                    for (int j = -1; j < tiles && ok; ++j) {
                         const bool more = j + 1 < tiles;
-                        DF2_WAIT(op_full(vr.slot), vr.phase);
-                        for (int s = 0; s < mt; ++s) {
-                            DF2_WAIT(p_full(s), cnt[s] & 1);
-                            ++cnt[s];
-                            tc_fence_after();
-                            pv(s, s, vr.slot, j == 0);
-                            if (s == mt - 1)
-                                commit(op_empty(vr.slot, 1));
-                            if (more) {
-                                if (s == 0) {
-                                    DF2_WAIT(op_full(kr.slot), kr.phase);
-                                    tc_fence_after();
-                                }
-                                qk(s, s, kr.slot);
-                            }
+                        if (j >= 0) {
+                            DF2_WAIT(op_full(vr.slot), vr.phase);
                         }
-                        vr.step(op_size);
+                        if (more) {
+                            DF2_WAIT(op_full(kr.slot), kr.phase);
+                        }
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (s == mt)
+                                break;
+                            if (j >= 0) {
+                                DF2_WAIT(p_full(s), cnt[s] & 1);
+                                ++cnt[s];
+                            } else {
+                                DF2_WAIT(q_full(s), q_phase[s]);
+                                q_phase[s] ^= 1u;
+                            }
+                            tc_fence_after();
+                            if (j >= 0)
+                                pv(s, s, vr.slot, j == 0);
+                            if (more)
+                                qk(s, s, kr.slot);
+                        }
+                        if (!ok)
+                            break;
+                        if (j >= 0) {
+                            commit(op_empty(vr.slot, 1));
+                            vr.step(op_size);
+                        }
                         if (more) {
                             commit(op_empty(kr.slot, 0));
                             kr.step(op_size);
                         }
                     }
                 } else {
+                    // the next S, then PV: the softmax always has an S waiting
                     DF2_WAIT(q_full(0), q_phase[0]);
                     q_phase[0] ^= 1u;
-                    DF2_WAIT(op_full(kr.slot), kr.phase);
-                    tc_fence_after();  // the queries in TMEM too
-                    qk(0, cnt[0] & 1, kr.slot);
-                    commit(op_empty(kr.slot, 0));
-                    kr.step(op_size);
-                    for (int j = 0; j < tiles; ++j) {
-                        const int sbuf = cnt[0] & 1;
-                        if (j + 1 < tiles) {
+#pragma unroll 1
+                    for (int j = 0; j <= tiles; ++j) {
+                        if (j < tiles) {
                             DF2_WAIT(op_full(kr.slot), kr.phase);
-                            tc_fence_after();
-                            qk(0, sbuf ^ 1, kr.slot);
+                            tc_fence_after();  // the queries in TMEM too
+                            qk(0, (cnt[0] + (j > 0 ? 1 : 0)) & 1, kr.slot);
                             commit(op_empty(kr.slot, 0));
                             kr.step(op_size);
                         }
-                        DF2_WAIT(op_full(vr.slot), vr.phase);
-                        DF2_WAIT(p_full(sbuf), (cnt[0] >> 1) & 1);
-                        ++cnt[0];
-                        tc_fence_after();
-                        pv(0, sbuf, vr.slot, j == 0);
-                        commit(op_empty(vr.slot, 1));
-                        vr.step(op_size);
+                        if (j > 0) {
+                            const int sbuf = cnt[0] & 1;
+                            DF2_WAIT(op_full(vr.slot), vr.phase);
+                            DF2_WAIT(p_full(sbuf), (cnt[0] >> 1) & 1);
+                            ++cnt[0];
+                            tc_fence_after();
+                            pv(0, sbuf, vr.slot, j == 1);
+                            commit(op_empty(vr.slot, 1));
+                            vr.step(op_size);
+                        }
                     }
                 }
                 seg_done(n);
@@ -694,107 +805,61 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             // every MMA issued must finish before TMEM is released (in a healthy run all have)
             commit(drain_bar);
             drain_wait(drain_bar, 0);
-        } else if (kQuant && warp >= 2) {
+        } else if (kQuant && warp == 2) {
             // ------------------------------------------------------------ scales of the keys and values
-            // The two warps take alternate tiles, a lane four keys: their pages, a turn later their
-            // scales, a turn later into shared memory as (ks, log2 vs, 1 / vs).  Two sets of registers
-            // take turns, so a turn never waits for the loads it has just issued.
-            const int ps = a.cache.page_size;
-            int base = 0;  // tiles of the CTA before the segment
+            // The producer brings a tile's scales as they lie; here they become (ks, log2 vs, 1 / vs).
+            int tcnt = 0;
             bool ok = true;
-            struct Turn {
-                int page[4];
-                float2 sc[4];
-            };
             for (int n = 0; ok; ++n) {
                 ok = seg_wait(n);
                 if (!ok || segs[n % SEGMENTS].tiles == 0)
                     break;
                 const Segment &g = segs[n % SEGMENTS];
-                const int tiles = g.tiles;
-                const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
-                auto held = [&](int j, int i) {
-                    const int tok = (g.tile + j) * BN + i * 32 + lane;
-                    return j < tiles && tok >= g.item.lo && tok < g.item.hi;
-                };
-                auto load_pages = [&](int j, Turn &t) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        t.page[i] = held(j, i) ? __ldg(pt + page_of_token(a, (g.tile + j) * BN + i * 32 + lane)) : -1;
-                };
-                auto load_scales = [&](int j, Turn &t) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        t.sc[i] = make_float2(0.f, -1.f);  // no key there
-                        if (held(j, i)) {
-                            const int tok = (g.tile + j) * BN + i * 32 + lane;
-                            const long long at = (static_cast<long long>(min(max(t.page[i], 0), a.cache.pages - 1)) *
-                                                      a.cache.heads + g.kvh) * ps + tok - page_of_token(a, tok) * ps;
-                            t.sc[i] = make_float2(__ldg(a.cache.k_scale + at), __ldg(a.cache.v_scale + at));
-                        }
-                    }
-                };
+                const int tiles = g.tiles, lo = g.item.lo - g.tile * BN, hi = g.item.hi - g.tile * BN;
                 float top_lv = -INFINITY;  // this lane's largest log2 of a value scale in the segment
-                // tile j from `now`, whose scales are on their way; `then` has the pages of tile j + 2
-                auto turn = [&](int j, Turn &now, Turn &then) {
-                    load_scales(j + 2, then);
-                    load_pages(j + 4, now);
-                    float lv[4], rv[4];
-                    bool zero = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float vs = now.sc[i].y;
-                        lv[i] = vs > 0.f ? __log2f(vs) : vs == 0.f ? -INFINITY : vs;
-                        rv[i] = vs != 0.f ? __frcp_rn(vs) : 0.f;
-                        if (vs > 0.f)
-                            top_lv = fmaxf(top_lv, lv[i]);
-                        zero |= vs == 0.f;
-                    }
-                    if (__any_sync(0xffffffffu, zero)) {
-                        // A row of zeros adds to l alone; any scale serves its codes.  One 2^60 below
-                        // the largest seen keeps it from setting m' (P' of the others would fall out of
-                        // f16) and its own P' far above float32's least.
-                        float ref = top_lv;
-                        for (int o = 16; o > 0; o >>= 1)
-                            ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (now.sc[i].y == 0.f) {
-                                lv[i] = fmaxf(floorf(ref) - 60.f, kLeastScale);
-                                rv[i] = exp2f(-lv[i]);
-                            }
-                    }
-                    // the first softmax warpgroup is done with the tile two back, so the second (which
-                    // the order of the MMAs keeps less than two tiles behind) with the one four back,
-                    // whose place this is
-                    const int at = base + j;
-                    if (at >= 2)
-                        ok = warp_wait(soft_done(at & 1), ((at >> 1) - 1) & 1, abort_flag);
+                for (int j = 0; j < tiles; ++j) {
+                    ok = warp_wait(raw_full(tcnt % kRaws), (tcnt / kRaws) & 1, abort_flag);
+                    // the first softmax warpgroup is done with the tile two back, so a second one (which
+                    // the order of the MMAs keeps less than two tiles behind) with the one four back:
+                    // the tile whose place this is
+                    if (ok && tcnt >= 2)
+                        ok = warp_wait(soft_done(tcnt & 1), ((tcnt >> 1) - 1) & 1, abort_flag);
                     if (!ok)
-                        return;
-                    float *sm = reinterpret_cast<float *>(smem + lay.scales) + (at % SCALES) * 3 * BN;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = i * 32 + lane;
-                        sm[k] = now.sc[i].x;
-                        sm[BN + k] = lv[i];
-                        sm[2 * BN + k] = rv[i];
+                        break;
+                    const float *raw = reinterpret_cast<const float *>(smem + lay.raw) + (tcnt % kRaws) * 2 * BN;
+                    float *sm = reinterpret_cast<float *>(smem + lay.scales) + (tcnt % kScales) * 3 * BN;
+#pragma unroll 1
+                    for (int k = lane; k < BN; k += 32) {
+                        const bool held = j * BN + k >= lo && j * BN + k < hi;
+                        const float ks = held ? raw[k] : 0.f, vs = held ? raw[BN + k] : 1.f;
+                        float lv = vs, rv = __fdividef(1.f, vs);
+                        if (vs > 0.f) {
+                            lv = __log2f(vs);
+                            if (held)
+                                top_lv = fmaxf(top_lv, lv);
+                        }
+                        if (__any_sync(0xffffffffu, vs == 0.f)) {
+                            // A row of zeros adds to l alone; any scale serves its codes.  One 2^60 below
+                            // the largest seen keeps it from setting m' (P' of the others would fall out
+                            // of f16) and its own P' far above float32's least.
+                            float ref = top_lv;
+                            for (int o = 16; o > 0; o >>= 1)
+                                ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+                            ref = fmaxf(floorf(ref) - 60.f, kLeastScale);
+                            if (vs == 0.f)
+                                lv = ref, rv = exp2f(-ref);
+                        }
+                        sm[k] = ks;
+                        sm[BN + k] = lv;
+                        sm[2 * BN + k] = rv;
                     }
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(scale_full(at % SCALES));
-                };
-                Turn x, y;
-                const int first = (warp ^ base) & 1;  // this warp's first tile of the segment
-                load_pages(first, x);
-                load_pages(first + 2, y);
-                load_scales(first, x);
-                for (int j = first; j < tiles && ok; j += 4) {
-                    turn(j, x, y);
-                    if (j + 2 < tiles && ok)
-                        turn(j + 2, y, x);
+                    if (lane == 0) {
+                        mbar_arrive(raw_empty(tcnt % kRaws));
+                        mbar_arrive(scale_full(tcnt % kScales));
+                    }
+                    ++tcnt;
                 }
-                base += tiles;
                 seg_done(n);
             }
         }
@@ -877,7 +942,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(fold_bar);
-            const bool met = __all_sync(0xffffffffu, mbar_wait(fold_bar, fold_phase, abort_flag));
+            const bool met = warp_wait(fold_bar, fold_phase, abort_flag);
             fold_phase ^= 1u;
             return met;
         };
@@ -909,20 +974,30 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     if (!ok)
                         break;
                     if constexpr (kQuant) {
-                        ok = warp_wait(scale_full(tcnt % SCALES), (tcnt / SCALES) & 1, abort_flag);
+                        ok = warp_wait(scale_full(tcnt % kScales), (tcnt / kScales) & 1, abort_flag);
                         if (!ok)
                             break;
                     }
                     tc_fence_after();
                     const uint32_t s_addr = lane_base + sbuf * BN;
-                    const uint32_t scales = sbase + lay.scales + ((tcnt % SCALES) * 3 * BN + col0) * 4;
+                    const uint32_t scales = sbase + lay.scales + ((tcnt % kScales) * 3 * BN + col0) * 4;
                     if (warp_live) {
                         // An 8-bit cache's scores of 128 keys do not fit the registers beside everything
-                        // else: they are read from TMEM (and scaled) twice.
+                        // else: scaled, they go back to TMEM until the maximum is known.
                         constexpr bool kKeep = !kQuant || kCols <= 64;
                         uint32_t v[kKeep ? kCols / 32 : 1][32];
                         const int rlo = lo - t0 - col0, rhi = hi - t0 - col0;
                         const bool edge = __any_sync(0xffffffffu, rlo > 0 || rhi < kCols);
+                        // keys c0 .. c0 + 31 that the row sees, a bit each; the others' scores go
+                        auto mask = [&](uint32_t(&x)[32], int c0) {
+                            const int below = min(max(rlo - c0, 0), 32), up_to = min(max(rhi - c0, 0), 32);
+                            const uint32_t seen = static_cast<uint32_t>((1ull << up_to) - 1) &
+                                                  ~static_cast<uint32_t>((1ull << below) - 1);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen & (1u << c)))
+                                    x[c] = 0xFF800000u;
+                        };
                         // x_j of 32 keys from c0 (of this copy's), their S taken out of TMEM into x
                         auto scores = [&](uint32_t(&x)[32], int c0) {
                             tmem_ld_32x32b_x32(s_addr + col0 + c0, x);
@@ -946,12 +1021,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             } else {
                                 tmem_wait_ld(x);
                             }
-                            if (edge) {
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    if (c0 + c < rlo || c0 + c >= rhi)
-                                        x[c] = 0xFF800000u;
-                            }
+                            if (edge)
+                                mask(x, c0);
                         };
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                         auto raise = [&](const uint32_t(&x)[32]) {
@@ -966,6 +1037,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             for (int i = 0; i < kCols / 32; ++i) {
                                 scores(v[kKeep ? i : 0], 32 * i);
                                 raise(v[kKeep ? i : 0]);
+                                if constexpr (!kKeep)
+                                    tmem_st_32x32b_x32(s_addr + col0 + 32 * i, v[0]);
                             }
                         } else {
 #pragma unroll
@@ -976,20 +1049,21 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 tmem_wait_ld(v[i]);
                             if (edge) {
 #pragma unroll
-                                for (int c = 0; c < kCols; ++c)
-                                    if (c < rlo || c >= rhi)
-                                        v[c / 32][c % 32] = 0xFF800000u;
+                                for (int i = 0; i < kCols / 32; ++i)
+                                    mask(v[i], 32 * i);
                             }
 #pragma unroll
                             for (int i = 0; i < kCols / 32; ++i)
                                 raise(v[i]);
                         }
+                        if constexpr (!kKeep)
+                            tmem_wait_st();
                         const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
                         const bool move = live && rise > LAZY;
                         if (j > 0 && __any_sync(0xffffffffu, move)) {
                             // the products so far must be in before they are scaled
-                            ok = __all_sync(0xffffffffu, mbar_wait(pv_done(s), (cnt - 1) & 1, abort_flag));
+                            ok = warp_wait(pv_done(s), (cnt - 1) & 1, abort_flag);
                             if (!ok)
                                 break;
                             tc_fence_after();
@@ -1030,8 +1104,10 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 for (int i = 0; i < 8; ++i)
                                     rv[i] = lds4(scales + (2 * BN + c0 + 4 * i) * 4);
                             }
-                            if constexpr (!kKeep)  // P goes where S has been read already
-                                scores(v[0], c0);
+                            if constexpr (!kKeep) {  // P goes where x has been read already
+                                tmem_ld_32x32b_x32(s_addr + col0 + c0, v[0]);
+                                tmem_wait_ld(v[0]);
+                            }
                             const uint32_t(&vc)[32] = v[kKeep ? c0 / 32 : 0];
 #pragma unroll
                             for (int c = 0; c < 32; c += 4) {
@@ -1119,7 +1195,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             float weight = 1.f;
             if constexpr (FOLD > 1) {
                 // the copies' common maximum; each copy's weight; the sum of their sums
-                float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold + BM * 32 * 4);
+                float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold + BM * 16 * 4);
                 ml[row] = make_float2(m * sl2, l);
                 ok = fold_sync();
                 if (!ok)
@@ -1143,40 +1219,48 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             }
             const float inv = whole ? (l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l) : 1.f;
             if (warp_live || FOLD > 1) {
+                constexpr int kChunk = FOLD > 1 ? 16 : 32;     // columns at a time
+                constexpr int kPer = kChunk / FOLD;            // ... of which this thread writes
+                const int k0 = FOLD > 1 ? row / kRows * kPer : 0;
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(lane_base + 256 + s * 128 + c, o);
-                    tmem_wait_ld(o);
-                    constexpr int kPer = 32 / FOLD;  // elements of the 32 that this thread writes
-                    int k0 = 0;
+                for (int c = 0; c < DP; c += kChunk) {
+                    uint32_t o[kChunk];
+                    const uint32_t src = lane_base + 256 + s * 128 + c;
                     if constexpr (FOLD > 1) {
-                        // through shared memory: rows of 32 words, word k of row r at k ^ (r mod 32)
+                        // through shared memory: rows of 16 words, word k of row r at k ^ (r / 2 mod 16)
+                        tmem_ld_32x32b_x16(src, o);
+                        tmem_wait_ld(o);
                         float *x = reinterpret_cast<float *>(smem + lay.fold);
+                        const int flip = (lane >> 1) & 15;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            x[row * 32 + (k ^ lane)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
+                        for (int k = 0; k < 16; ++k)
+                            x[row * 16 + (k ^ flip)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
                         ok = ok && fold_sync();
-                        k0 = row / kRows * kPer;
 #pragma unroll
                         for (int k = 0; k < kPer; ++k) {
                             float sum = 0.f;
 #pragma unroll
                             for (int f = 0; f < FOLD; ++f)
-                                sum += x[(f * kRows + trow) * 32 + ((k0 + k) ^ lane)];
+                                sum += x[(f * kRows + trow) * 16 + ((k0 + k) ^ flip)];
                             o[k] = __float_as_uint(sum);
                         }
                         ok = ok && fold_sync();
+                    } else {
+                        tmem_ld_32x32b_x32(src, o);
+                        tmem_wait_ld(o);
                     }
                     if (live && whole) {
+                        auto pack = [&](int k) { return bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv); };
+                        if constexpr (kPer >= 8) {
 #pragma unroll
-                        for (int k = 0; k < kPer; k += 8)
-                            if (c + k0 + k < dim)
-                                *reinterpret_cast<uint4 *>(dst + c + k0 + k) = make_uint4(
-                                    bf16_pack(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv),
-                                    bf16_pack(__uint_as_float(o[k + 2]) * inv, __uint_as_float(o[k + 3]) * inv),
-                                    bf16_pack(__uint_as_float(o[k + 4]) * inv, __uint_as_float(o[k + 5]) * inv),
-                                    bf16_pack(__uint_as_float(o[k + 6]) * inv, __uint_as_float(o[k + 7]) * inv));
+                            for (int k = 0; k < kPer; k += 8)
+                                if (c + k0 + k < dim)
+                                    *reinterpret_cast<uint4 *>(dst + c + k0 + k) =
+                                        make_uint4(pack(k), pack(k + 2), pack(k + 4), pack(k + 6));
+                        } else {
+                            if (c + k0 < dim)
+                                *reinterpret_cast<uint2 *>(dst + c + k0) = make_uint2(pack(0), pack(2));
+                        }
                     } else if (live) {
 #pragma unroll
                         for (int k = 0; k < kPer; k += 4)
@@ -1215,9 +1299,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             const int t = threadIdx.x & 127;
             const int dim = a.cache.dim;
             constexpr int kChunks = DP / 16;
-            // operand 2 j is tile j's K, 2 j + 1 its V; operand i is in slot i mod size of a ring, for
-            // the (i / size)-th time
-            int rslot = kv, rround = 0, wslot = kv, wround = 0;
+            RingSlot rs{kv, 0}, ws{kv, 0};  // in the TMA ring, in the widened one
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 ok = seg_wait(n);
@@ -1227,63 +1309,58 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 const int tiles = g.tiles, first = g.tile * BN, item_lo = g.item.lo, item_hi = g.item.hi;
                 for (int j = 0; j < tiles && ok; ++j) {
                     const int t0 = first + j * BN;
-                    // the n-th time (from 0) that this warpgroup takes over the slot, -1: it was free
-                    const int turn = kWide % 2 == 0 ? wround - 1 : (wround >> 1) - (kv == 0 ? wslot != 1 : wslot == 1);
+                    const int turn = ws.turn(kWide, kv);
                     if (turn >= 0)
-                        ok = warp_wait(wide_empty(wslot, kv), turn & 1, abort_flag);
+                        ok = warp_wait(wide_empty(ws.slot, kv), turn & 1, abort_flag);
                     if (!ok)
                         break;
-                    const uint32_t r_phase = rround >> (a.ring & 1) & 1;
-                    ok = warp_wait(ring_full(rslot, kv), r_phase, abort_flag);
+                    const uint32_t r_phase = rs.round >> (a.ring & 1) & 1;
+                    ok = warp_wait(ring_full(rs.slot, kv), r_phase, abort_flag);
                     if (!ok)
                         break;
-                    const uint8_t *src = smem + lay.ring + rslot * lay.ring_stage;
-                    uint8_t *dst = smem + lay.wide + wslot * kTile;
+                    const uint8_t *src = smem + lay.ring + rs.slot * lay.ring_stage;
+                    uint8_t *dst = smem + lay.wide + ws.slot * kTile;
                     // sixteen codes at a time; a code of zero is the number zero in both types
-                    uint4 v[kChunks];
-#pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int r = i * (128 / kChunks) + t / kChunks, c = t % kChunks;
-                        v[i] = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
-                    }
                     const int c = t % kChunks, odd = c >> 2, c0 = 2 * (c & 3);
-                    if (t0 < item_lo || t0 + BN > item_hi || c * 16 >= dim) {
+                    const bool edge = t0 < item_lo || t0 + BN > item_hi || c * 16 >= dim;
+#pragma unroll 1
+                    for (int r0 = t / kChunks; r0 < BN; r0 += 4 * (128 / kChunks)) {
+                        uint4 v[4];
 #pragma unroll
-                        for (int i = 0; i < kChunks; ++i) {
-                            const int r = i * (128 / kChunks) + t / kChunks;
-                            if (t0 + r < item_lo || t0 + r >= item_hi || c * 16 >= dim)
-                                v[i] = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + i * (128 / kChunks);
+                            v[i] = *reinterpret_cast<const uint4 *>(src + r * dim + c * 16);
                         }
-                    }
+                        if (edge) {
 #pragma unroll
-                    for (int i = 0; i < kChunks; ++i) {
-                        const int r = i * (128 / kChunks) + t / kChunks;
-                        // lanes of the two halves write opposite chunks of a pair, so eight lanes
-                        // cover all banks
-                        const uint2 w0 = widen4<TYPE>(odd ? v[i].z : v[i].x), w1 = widen4<TYPE>(odd ? v[i].w : v[i].y),
-                                    w2 = widen4<TYPE>(odd ? v[i].x : v[i].z), w3 = widen4<TYPE>(odd ? v[i].y : v[i].w);
-                        uint8_t *d = dst + odd * HALF_BYTES + r * 128;
-                        *reinterpret_cast<uint4 *>(d + (((c0 + odd) ^ (r & 7)) << 4)) =
-                            make_uint4(w0.x, w0.y, w1.x, w1.y);
-                        *reinterpret_cast<uint4 *>(d + (((c0 + 1 - odd) ^ (r & 7)) << 4)) =
-                            make_uint4(w2.x, w2.y, w3.x, w3.y);
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = r0 + i * (128 / kChunks);
+                                if (t0 + r < item_lo || t0 + r >= item_hi || c * 16 >= dim)
+                                    v[i] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + i * (128 / kChunks);
+                            // lanes of the two halves write opposite chunks of a pair, so eight lanes
+                            // cover all banks
+                            const uint2 w0 = widen4<TYPE>(odd ? v[i].z : v[i].x), w1 = widen4<TYPE>(odd ? v[i].w : v[i].y),
+                                        w2 = widen4<TYPE>(odd ? v[i].x : v[i].z), w3 = widen4<TYPE>(odd ? v[i].y : v[i].w);
+                            uint8_t *d = dst + odd * HALF_BYTES + r * 128;
+                            *reinterpret_cast<uint4 *>(d + (((c0 + odd) ^ (r & 7)) << 4)) =
+                                make_uint4(w0.x, w0.y, w1.x, w1.y);
+                            *reinterpret_cast<uint4 *>(d + (((c0 + 1 - odd) ^ (r & 7)) << 4)) =
+                                make_uint4(w2.x, w2.y, w3.x, w3.y);
+                        }
                     }
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(ring_empty(rslot));
-                        mbar_arrive(wide_full(wslot));
+                        mbar_arrive(ring_empty(rs.slot, a.ring & 1 ? 1 - kv : kv));
+                        mbar_arrive(wide_full(ws.slot));
                     }
-                    rslot += 2;
-                    if (rslot >= a.ring) {
-                        rslot -= a.ring;
-                        ++rround;
-                    }
-                    wslot += 2;
-                    if (wslot >= kWide) {
-                        wslot -= kWide;
-                        ++wround;
-                    }
+                    rs.step(a.ring);
+                    ws.step(kWide);
                 }
                 seg_done(n);
             }
@@ -1516,8 +1593,10 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     c.records = a.records;
     c.part_ml = a.part_ml;
     c.part_o = a.part_o;
-    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), static_cast<unsigned>(c.rows / 8)),
-                            dim3(256), 0, stream, c);
+    // the rows that an item can have, eight to a CTA
+    const long long most = tiles == 2 ? c.rows : std::min<long long>(a.tpm, tokens.max_new) * a.group;
+    const unsigned y = static_cast<unsigned>((most + 7) / 8);
+    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), y), dim3(256), 0, stream, c);
 }
 
 }  // namespace df2

@@ -109,6 +109,14 @@ __device__ __forceinline__ void fence_proxy_async()
 
 // ---------------------------------------------------------------- TMA
 
+// `bytes` consecutive bytes (a multiple of 16, both addresses 16-byte aligned), completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // A box of a 4-D tensor (x = innermost element coordinate; x * element size a multiple of 16).
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z,
                                             int w)
