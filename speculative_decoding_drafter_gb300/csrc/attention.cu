@@ -102,11 +102,15 @@ __device__ __forceinline__ Sequence sequence_at(const Args &a, const Sequence *n
     return b < NEAR ? near[b] : load_sequence(a, b);
 }
 
+constexpr int ITEM_COST = 1;
+
 struct Item {
     int tok0, ntok;    // first token in its sequence, tokens
     int p0;            // position of the first
     int lo, hi;        // positions some row sees
     int tile0, tiles;  // key tiles (one, empty, if nothing is seen)
+
+    __device__ __forceinline__ int units() const { return tiles + ITEM_COST; }
 };
 
 __device__ __forceinline__ Item item_at(const Args &a, const Sequence &s, int qt)
@@ -139,20 +143,41 @@ struct Segment {
     int end_cta;         // of an item that begins here and ends elsewhere: the CTA with its last tile
 };
 
-// The segments of a CTA's share [u, u_end) of the units (cache head by cache head, item by item).
+__device__ __forceinline__ long long quotient(long long a, int b)
+{
+    return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// `units` cut into `grid` shares, share c beginning at floor(c units / grid).
+struct Shares {
+    long long units, each;
+    int grid, more;
+
+    __device__ __forceinline__ Shares(long long n, int g) : units(n), each(quotient(n, g)), grid(g)
+    {
+        more = static_cast<int>(n - each * g);
+    }
+    __device__ __forceinline__ long long begin(int c) const { return c * each + static_cast<unsigned>(c * more) / static_cast<unsigned>(grid); }
+    __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * grid - 1) / units); }
+};
+
+// The segments of a CTA's share [u, u_end) of the units, cache head by cache head, item by item.  An
+// item has a unit for each key tile and, before them, ITEM_COST for its queries, its first score and
+// its results: CTAs with short items would else finish last.
 // One warp walks and hands the segments to the others through shared memory: walking code in every
 // role made the loops too long for the instruction cache (warps waited for instructions half the time).
 struct Walk {
-    long long u, u_begin, u_end;
+    long long u, u_end;
+    int pieces = 0;
     int b, kvh, qt, off, nq;
     Sequence s;
     const Sequence *near;
 
-    __device__ __forceinline__ void begin(const Args &a, const Sequence *near_, const int *prefix, long long units, int grid, int c)
+    __device__ __forceinline__ void begin(const Args &a, const Sequence *near_, const int *prefix, const Shares &shares, int c)
     {
         near = near_;
-        u = u_begin = c * units / grid;
-        u_end = (c + 1) * units / grid;
+        u = shares.begin(c);
+        u_end = shares.begin(c + 1);
         int lo = 0, hi = a.tokens.B;  // the largest b with prefix[b] * heads <= u
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -164,50 +189,54 @@ struct Walk {
         b = lo;
         s = sequence_at(a, near, b);
         nq = items_of(a, s);
-        const int per_head = max(prefix[b + 1] - prefix[b], 1);
-        const int r = static_cast<int>(u - static_cast<long long>(prefix[b]) * a.cache.heads);
-        kvh = r / per_head;
-        off = r - kvh * per_head;
+        const unsigned per_head = max(prefix[b + 1] - prefix[b], 1);
+        const unsigned r = static_cast<unsigned>(u - static_cast<long long>(prefix[b]) * a.cache.heads);
+        kvh = static_cast<int>(r / per_head);
+        off = static_cast<int>(r - kvh * per_head);
         for (qt = 0; qt + 1 < nq; ++qt) {
-            const int t = item_at(a, s, qt).tiles;
+            const int t = item_at(a, s, qt).units();
             if (off < t)
                 break;
             off -= t;
         }
     }
 
-    __device__ __forceinline__ bool next(const Args &a, int cta, long long units, int grid, Segment &g)
+    __device__ __forceinline__ void next(const Args &a, int cta, const Shares &shares, Segment &g)
     {
-        if (u >= u_end) {
-            g.tiles = 0;
-            return false;
-        }
-        while (kvh == a.cache.heads) {  // the next sequence that has tokens
-            ++b;
-            s = sequence_at(a, near, b);
-            nq = items_of(a, s);
-            kvh = nq > 0 ? 0 : a.cache.heads;
-        }
-        g.item = item_at(a, s, qt);
-        g.b = b;
-        g.kvh = kvh;
-        g.start = s.start;
-        g.slot = 2 * cta + (u != u_begin ? 1 : 0);
-        g.tile = g.item.tile0 + off;
-        g.tiles = static_cast<int>(min(static_cast<long long>(g.item.tiles - off), u_end - u));
-        g.first = off == 0;
-        g.end_cta = static_cast<int>(((u - off + g.item.tiles) * grid - 1) / units);
-        u += g.tiles;
-        off += g.tiles;
-        g.last = off == g.item.tiles;
-        if (g.last) {
-            off = 0;
-            if (++qt == nq) {
-                qt = 0;
-                ++kvh;
+        g.tiles = 0;
+        while (g.tiles == 0 && u < u_end) {
+            while (kvh == a.cache.heads) {  // the next sequence that has tokens
+                ++b;
+                s = sequence_at(a, near, b);
+                nq = items_of(a, s);
+                kvh = nq > 0 ? 0 : a.cache.heads;
+            }
+            g.item = item_at(a, s, qt);
+            g.b = b;
+            g.kvh = kvh;
+            g.start = s.start;
+            const int n = static_cast<int>(min(static_cast<long long>(g.item.units() - off), u_end - u));
+            const int from = max(off - ITEM_COST, 0), to = off + n - ITEM_COST;
+            u += n;
+            off += n;
+            if (to > from) {
+                g.tile = g.item.tile0 + from;
+                g.tiles = to - from;
+                g.first = from == 0;
+                g.last = to == g.item.tiles;
+                g.slot = 2 * cta + pieces++;
+                if (g.first && !g.last)
+                    g.end_cta = shares.owner(u - off + g.item.units() - 1);
+            }
+            if (off == g.item.units()) {
+                off = 0;
+                if (++qt == nq) {
+                    qt = 0;
+                    ++kvh;
+                }
             }
         }
-        return true;
+        pieces = min(pieces, 1);  // only a CTA's first and last segments can be pieces
     }
 };
 
@@ -286,9 +315,9 @@ struct Shape {
     static constexpr int kThreads = 128 * (1 + QT + (TYPE ? 2 : 0));
     // registers of a thread after the roles part: control, softmax, widening (their sum times 128
     // is at most what the launch holds: 65536 / threads, a multiple of 8, times the threads)
-    static constexpr int kSoftRegs = TYPE == 0 ? 208 : QT == 2 ? 128 : 184;
-    static constexpr int kWideRegs = QT == 2 ? 72 : 112;
-    static constexpr int kControlRegs = TYPE == 0 ? 88 : QT == 2 ? 80 : 104;
+    static constexpr int kSoftRegs = TYPE == 0 ? 200 : QT == 2 ? 128 : 184;
+    static constexpr int kWideRegs = QT == 2 ? 64 : 112;
+    static constexpr int kControlRegs = TYPE == 0 ? 104 : QT == 2 ? 96 : 104;
     static constexpr bool kSplitRegs = kThreads > 256;
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static_assert(!kSplitRegs || kControlRegs + QT * kSoftRegs + (TYPE ? 2 * kWideRegs : 0) <=
@@ -412,13 +441,15 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     auto pv_done = [&](int s) { return bar0 + 8u * (kRest + 4 + s); };
     auto q_full = [&](int s) { return bar0 + 8u * (kRest + 6 + s); };
     auto scale_full = [&](int s) { return bar0 + 8u * (kRest + 8 + s); };
-    const uint32_t drain_bar = bar0 + 8u * (kRest + 8 + MAX_SCALES);
-    const uint32_t fold_bar = bar0 + 8u * (kRest + 9 + MAX_SCALES);
-    auto soft_done = [&](int x) { return bar0 + 8u * (kRest + 10 + MAX_SCALES + x); };
-    auto seg_full = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + i); };
-    auto seg_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + SEGMENTS + i); };
-    auto raw_full = [&](int i) { return bar0 + 8u * (kRest + 12 + MAX_SCALES + 2 * SEGMENTS + i); };
-    auto raw_empty = [&](int i) { return bar0 + 8u * (kRest + 12 + 2 * MAX_SCALES + 2 * SEGMENTS + i); };
+    constexpr int kMore = kRest + 8 + MAX_SCALES;
+    const uint32_t drain_bar = bar0 + 8u * kMore;
+    const uint32_t meet_bar = bar0 + 8u * (kMore + 1);
+    auto soft_done = [&](int x) { return bar0 + 8u * (kMore + 2 + x); };
+    auto seg_full = [&](int i) { return bar0 + 8u * (kMore + 4 + i); };
+    auto seg_empty = [&](int i) { return bar0 + 8u * (kMore + 4 + SEGMENTS + i); };
+    auto raw_full = [&](int i) { return bar0 + 8u * (kMore + 4 + 2 * SEGMENTS + i); };
+    auto raw_empty = [&](int i) { return bar0 + 8u * (kMore + 4 + 2 * SEGMENTS + MAX_SCALES + i); };
+    static_assert(kMore + 4 + 2 * SEGMENTS + 2 * MAX_SCALES == BAR_COUNT, "barriers");
     // what the MMAs read: the TMA ring itself, or the widened one
     const int op_size = kQuant ? kWide : a.ring;
     const uint32_t op_base = sbase + (kQuant ? lay.wide : lay.ring);
@@ -463,7 +494,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_init(seg_empty(s), 2 + 4 * QT + (kQuant ? 1 + 8 : 0));  // warps that read it
         }
         mbar_init(drain_bar, 1);
-        mbar_init(fold_bar, 4);
+        mbar_init(meet_bar, 4);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&map_k);
@@ -473,61 +504,50 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-    griddep_wait();
-
-    // key tiles of each sequence (for one cache head), then their running sum
-    const int B = a.tokens.B;
-    if (B <= kThreads / 32) {
-        if (warp < B) {
-            const Sequence s = load_sequence(a, warp);
-            if (lane == 0)
-                near[warp] = s;
-            const int nq = items_of(a, s);
-            int t = 0;
-            for (int qt = lane; qt < nq; qt += 32)
-                t += item_at(a, s, qt).tiles;
-            for (int o = 16; o > 0; o >>= 1)
-                t += __shfl_xor_sync(0xffffffffu, t, o);
-            if (lane == 0)
-                prefix[warp + 1] = t;
-        }
-    } else {
-        for (int b = threadIdx.x; b < B; b += kThreads) {
-            const Sequence s = load_sequence(a, b);
-            if (b < NEAR)
-                near[b] = s;
-            const int nq = items_of(a, s);
-            int t = 0;
-            for (int qt = 0; qt < nq; ++qt)
-                t += item_at(a, s, qt).tiles;
-            prefix[b + 1] = t;
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int sum = 0;
-        if (lane == 0)
-            prefix[0] = 0;
-        for (int b0 = 0; b0 < B; b0 += 32) {
-            int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, t, o);
-                t += lane >= o ? x : 0;
-            }
-            t += sum;
-            if (b0 + lane < B)
-                prefix[b0 + lane + 1] = t;
-            sum = __shfl_sync(0xffffffffu, t, 31);
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const long long units = static_cast<long long>(prefix[B]) * a.cache.heads;
-    const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), units));
+    griddep_wait();
+
+    // Key tiles of each sequence (for one cache head), then, in warp 0, their running sum.  Up to 32
+    // sequences warp 0 does it alone and the others need not wait.
+    const int B = a.tokens.B;
+    auto tiles_of = [&](const Sequence &s, int first, int step) {
+        const int nq = items_of(a, s);
+        int t = 0;
+        for (int qt = first; qt < nq; qt += step)
+            t += item_at(a, s, qt).units();
+        return t;
+    };
+    if (B > NEAR) {
+        for (int b = threadIdx.x; b < B; b += kThreads) {
+            const Sequence s = load_sequence(a, b);
+            if (b < NEAR)
+                near[b] = s;
+            prefix[b + 1] = tiles_of(s, 0, 1);
+        }
+        __syncthreads();
+    } else if (warp == 0) {
+        Sequence s{0, 0, 0};
+        if (lane < B)
+            near[lane] = s = load_sequence(a, lane);
+        if (__all_sync(0xffffffffu, items_of(a, s) <= 4)) {
+            if (lane < B)
+                prefix[lane + 1] = tiles_of(s, 0, 1);
+        } else {
+            __syncwarp();
+            for (int b = 0; b < B; ++b) {
+                int t = tiles_of(near[b], lane, 32);
+                for (int o = 16; o > 0; o >>= 1)
+                    t += __shfl_xor_sync(0xffffffffu, t, o);
+                if (lane == 0)
+                    prefix[b + 1] = t;
+            }
+        }
+        __syncwarp();
+    }
     const int cta = blockIdx.x;
-    const bool works = cta < grid;
     Segment *segs = reinterpret_cast<Segment *>(smem + lay.segs);
     // the CTA's n-th segment (tiles == 0: there is none), and done with it
     auto seg_wait = [&](int n) { return warp_wait(seg_full(n % SEGMENTS), (n / SEGMENTS) & 1, abort_flag); };
@@ -537,10 +557,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_arrive(seg_empty(n % SEGMENTS));
     };
 
-    if (!works) {
-        if (threadIdx.x == 0)
-            a.records[cta].valid = 0;
-    } else if (warp == 0 || warp == 3) {
+    if (warp == 0 || warp == 3) {
         // ---------------------------------------------------------------- TMA producers: K, V
         // Warp 0 also walks.  One lane issues with warp-uniform operands, box after box: lanes that
         // issue their own boxes are taken one by one anyhow, at several times the cost.
@@ -549,9 +566,32 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         const int kv = warp == 0 ? 0 : 1;
         const CUtensorMap *map = kv ? &map_v : &map_k;
         const float *scale_base = kv ? a.cache.v_scale : a.cache.k_scale;
+        long long units = 0;
+        if (kv == 0) {
+            int sum = 0;
+            if (lane == 0)
+                prefix[0] = 0;
+            for (int b0 = 0; b0 < B; b0 += 32) {
+                int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, t, o);
+                    t += lane >= o ? x : 0;
+                }
+                t += sum;
+                if (b0 + lane < B)
+                    prefix[b0 + lane + 1] = t;
+                sum = __shfl_sync(0xffffffffu, t, 31);
+            }
+            __syncwarp();
+            units = static_cast<long long>(sum) * a.cache.heads;
+        }
+        const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(units, 1ll)));
+        const Shares shares(units, grid);
         Walk walk;
-        if (kv == 0)
-            walk.begin(a, near, prefix, units, grid, cta);
+        if (kv == 0 && cta < grid && units > 0)
+            walk.begin(a, near, prefix, shares, cta);
+        else
+            walk.u = walk.u_end = 0;
         const int boxes = BN / a.box, per_batch = 32 / boxes;  // boxes of a tile, tiles of a batch of 32
         const int ps = a.cache.page_size, dim = a.cache.dim;
         const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
@@ -566,7 +606,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 if (!ok)
                     break;
                 Segment next;
-                walk.next(a, cta, units, grid, next);
+                walk.next(a, cta, shares, next);
                 if (lane == 0) {
                     segs[n % SEGMENTS] = next;
                     mbar_arrive(seg_full(n % SEGMENTS));
@@ -758,17 +798,18 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 q_phase[s] ^= 1u;
                             }
                             tc_fence_after();
-                            if (j >= 0)
+                            if (j >= 0) {
                                 pv(s, s, vr.slot, j == 0);
+                                if (s == mt - 1)
+                                    commit(op_empty(vr.slot, 1));
+                            }
                             if (more)
                                 qk(s, s, kr.slot);
                         }
                         if (!ok)
                             break;
-                        if (j >= 0) {
-                            commit(op_empty(vr.slot, 1));
+                        if (j >= 0)
                             vr.step(op_size);
-                        }
                         if (more) {
                             commit(op_empty(kr.slot, 0));
                             kr.step(op_size);
@@ -936,14 +977,14 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 mbar_arrive(q_full(s));
         };
 
-        // all four warps of the (one) softmax warpgroup meet; false on a timeout
-        uint32_t fold_phase = 0;
-        auto fold_sync = [&]() {
+        // the four warps of the (one) softmax warpgroup meet; false on a timeout
+        uint32_t meet_phase = 0;
+        auto group_sync = [&]() {
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(fold_bar);
-            const bool met = warp_wait(fold_bar, fold_phase, abort_flag);
-            fold_phase ^= 1u;
+                mbar_arrive(meet_bar);
+            const bool met = warp_wait(meet_bar, meet_phase, abort_flag);
+            meet_phase ^= 1u;
             return met;
         };
 
@@ -1197,7 +1238,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 // the copies' common maximum; each copy's weight; the sum of their sums
                 float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold + BM * 16 * 4);
                 ml[row] = make_float2(m * sl2, l);
-                ok = fold_sync();
+                ok = group_sync();
                 if (!ok)
                     break;
                 float top = -INFINITY;
@@ -1235,7 +1276,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             x[row * 16 + (k ^ flip)] = weight == 0.f ? 0.f : __uint_as_float(o[k]) * weight;
-                        ok = ok && fold_sync();
+                        ok = ok && group_sync();
 #pragma unroll
                         for (int k = 0; k < kPer; ++k) {
                             float sum = 0.f;
@@ -1244,7 +1285,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 sum += x[(f * kRows + trow) * 16 + ((k0 + k) ^ flip)];
                             o[k] = __float_as_uint(sum);
                         }
-                        ok = ok && fold_sync();
+                        ok = ok && group_sync();
                     } else {
                         tmem_ld_32x32b_x32(src, o);
                         tmem_wait_ld(o);
@@ -1378,69 +1419,71 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
         atomicOr(a.status, kStatusTimeoutAttention);
 }
 
-struct CombineArgs {
-    HeadRows out;
-    float *lse;
-    int q_heads, group, tpm, dim, rows;
-    const SplitRecord *records;
-    const float2 *part_ml;
-    const float *part_o;
-};
-
-// Joins the pieces of the items that several CTAs worked on: a warp a row, in CTA order.
-__global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a)
+// Joins the pieces of the items that several CTAs worked on, in CTA order: a warp a row, a lane
+// four dimensions.  It is a chain of loads (the record, then the pieces' maxima and sums), so the
+// first pieces of o are asked for before their weights are known.
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Args a, int rows)
 {
+    constexpr int kEarly = 8;
     griddep_launch_dependents();
     griddep_wait();
     const SplitRecord rec = a.records[blockIdx.x];
     const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int tile = row / BM, r = row % BM, rt = r / a.group, gi = r - rt * a.group;
-    const int t = tile * a.tpm + rt;
+    const int t = tile * a.tpm + rt, dim = a.cache.dim;
     if (!rec.valid || rt >= a.tpm || t >= rec.ntok)
         return;
     const int n = rec.c1 - rec.c0 + 1;
-    auto at = [&](int i) {
-        const int slot = i == 0 ? rec.first_slot : 2 * (rec.c0 + i);
-        return static_cast<long long>(slot) * a.rows + row;
+    auto at = [&](int i) { return static_cast<long long>(i == 0 ? rec.first_slot : 2 * (rec.c0 + i)) * rows + row; };
+    auto piece = [&](int i) {
+        return i < n && 4 * lane < dim ? *reinterpret_cast<const float4 *>(a.part_o + at(i) * dim + 4 * lane)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32)
+    float4 early[kEarly];
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+        early[i] = piece(i);
+    float2 ml = lane < n ? a.part_ml[at(lane)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+    for (int i = lane + 32; i < n; i += 32)
         top = fmaxf(top, a.part_ml[at(i)].x);
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float base = top == -INFINITY ? 0.f : top;
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float w, const float4 &o) {
+        acc.x = fmaf(w, o.x, acc.x), acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z), acc.w = fmaf(w, o.w, acc.w);
+    };
     for (int i0 = 0; i0 < n; i0 += 32) {
-        float wgt = 0.f;
-        if (i0 + lane < n) {
-            const float2 ml = a.part_ml[at(i0 + lane)];
-            wgt = exp2f(ml.x - base);
-            // in one power: with an 8-bit cache the maximum carries a value's scale, and the weight
-            // alone may fall below what float32 holds
-            l += ml.y > 0.f ? exp2f(ml.x - base + log2f(ml.y)) : ml.y == 0.f ? 0.f : ml.y;
+        if (i0 > 0)
+            ml = i0 + lane < n ? a.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
+        const float wgt = exp2f(ml.x - base);
+        // in one power: with an 8-bit cache the maximum carries a value's scale, and the weight
+        // alone may fall below what float32 holds
+        l += ml.y > 0.f ? exp2f(ml.x - base + log2f(ml.y)) : ml.y == 0.f ? 0.f : ml.y;
+        int i = 0;
+        if (i0 == 0) {
+#pragma unroll
+            for (; i < kEarly; ++i)
+                add(__shfl_sync(0xffffffffu, wgt, i), early[i]);
         }
         const int m = min(32, n - i0);
 #pragma unroll 4
-        for (int i = 0; i < m; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wgt, i);
-            if (4 * lane < a.dim) {
-                const float4 o = *reinterpret_cast<const float4 *>(a.part_o + at(i0 + i) * a.dim + 4 * lane);
-                acc.x = fmaf(wi, o.x, acc.x), acc.y = fmaf(wi, o.y, acc.y);
-                acc.z = fmaf(wi, o.z, acc.z), acc.w = fmaf(wi, o.w, acc.w);
-            }
-        }
+        for (; i < m; ++i)
+            add(__shfl_sync(0xffffffffu, wgt, i), piece(i0 + i));
     }
     for (int o = 16; o > 0; o >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    const long long tok = rec.tok0 + t;
+    const long long token = rec.tok0 + t;
     const int head = rec.kvh * a.group + gi;
-    if (4 * lane < a.dim)
-        *reinterpret_cast<uint2 *>(a.out.data + tok * a.out.token_stride + head * a.out.head_stride + 4 * lane) =
+    if (4 * lane < dim)
+        *reinterpret_cast<uint2 *>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * lane) =
             make_uint2(bf16_pack(acc.x * inv, acc.y * inv), bf16_pack(acc.z * inv, acc.w * inv));
     if (a.lse && lane == 0)
-        a.lse[tok * a.q_heads + head] = (top + log2f(l)) * 0.69314718055994530942f;
+        a.lse[token * a.q.heads + head] = (top + log2f(l)) * 0.69314718055994530942f;
 }
 
 // Row tiles an item has: two when some sequence may have more rows than one holds.
@@ -1582,21 +1625,10 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     e = cache.dim <= 64 ? launch_rows<64>(a, tiles, fold, sms, stream) : launch_rows<128>(a, tiles, fold, sms, stream);
     if (e != cudaSuccess)
         return e;
-    CombineArgs c{};
-    c.out = out;
-    c.lse = lse;
-    c.q_heads = q.heads;
-    c.group = a.group;
-    c.tpm = a.tpm;
-    c.dim = cache.dim;
-    c.rows = tiles * BM;
-    c.records = a.records;
-    c.part_ml = a.part_ml;
-    c.part_o = a.part_o;
     // the rows that an item can have, eight to a CTA
-    const long long most = tiles == 2 ? c.rows : std::min<long long>(a.tpm, tokens.max_new) * a.group;
+    const long long most = tiles == 2 ? 2 * BM : std::min<long long>(a.tpm, tokens.max_new) * a.group;
     const unsigned y = static_cast<unsigned>((most + 7) / 8);
-    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), y), dim3(256), 0, stream, c);
+    return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), y), dim3(256), 0, stream, a, tiles * BM);
 }
 
 }  // namespace df2
