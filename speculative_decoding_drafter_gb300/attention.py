@@ -157,17 +157,21 @@ class _Plan:
 
     def _bind(self, args, keep, outputs, stream):
         self._fn = getattr(library(), self._name)
+        self._device = torch.cuda.current_device()
         self._args, self._keep, self.outputs = args, keep, outputs
         self._handle = None if stream is None else _stream(stream)
 
     def __call__(self):
         handle = self._handle
-        if handle is None:
-            handle = torch.cuda.current_stream().cuda_stream
-        st = self._fn(*self._args, handle)
+        st = self._fn(*self._args, _current_stream(self._device) if handle is None else handle)
         if st:
             raise DFlash2Error(st, self._name)
         return self.outputs
+
+
+# the raw handle without building a stream object, which costs as much as the launch
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _out_like(x):

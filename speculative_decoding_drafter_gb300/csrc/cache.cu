@@ -18,6 +18,7 @@
 
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -40,10 +41,21 @@ struct RowsArgs {
     int N, dim;
     float sine_sign;
     int rows;            // rows of a token: q heads, then cache heads of k, then of v
-    int units_per_token;
+    int rows_per_unit, units_per_token;
     int vec_table;  // cosines and sines in 16-byte loads
     int shuffle;    // half layout: partners are whole chunks of other lanes
 };
+
+// Row h of token n: of q, then of k, then of v.
+template <bool CACHE>
+__device__ __forceinline__ const uint16_t *source_row(const RowsArgs &a, int n, int h)
+{
+    const int qh = a.q.heads, kvh = CACHE ? a.cache.heads : 0;
+    if (!CACHE || h < qh)
+        return a.q.data + n * a.q.token_stride + h * a.q.head_stride;
+    const HeadRows &s = h < qh + kvh ? a.k : a.v;
+    return s.data + n * s.token_stride + (h - (h < qh + kvh ? qh : qh + kvh)) * s.head_stride;
+}
 
 // Cosines and signed sines of the 8 elements of chunk `c`.
 __device__ __forceinline__ void load_turn(const RowsArgs &a, int pos, int c, float (&cs)[8], float (&sn)[8])
@@ -87,9 +99,9 @@ __device__ __forceinline__ void load_turn(const RowsArgs &a, int pos, int c, flo
     }
 }
 
-// x (8 elements of chunk c of the row at `row`) turned in place.  All lanes of the warp call it.
-template <int LG>
-__device__ __forceinline__ void turn(const RowsArgs &a, const uint16_t *row, const uint4 &raw, bool live, int c, int lane,
+// x (8 elements of chunk c of row h of token n) turned in place.  All lanes of the warp call it.
+template <int LG, bool CACHE>
+__device__ __forceinline__ void turn(const RowsArgs &a, int n, int h, const uint4 &raw, bool live, int c, int lane,
                                      const float (&cs)[8], const float (&sn)[8], float (&x)[8])
 {
     const int rot = a.rope.rot, half = rot / 2;
@@ -109,16 +121,21 @@ __device__ __forceinline__ void turn(const RowsArgs &a, const uint16_t *row, con
             p[2 * i] = bf16_lo(o), p[2 * i + 1] = bf16_hi(o);
         }
     } else {  // pairs that start inside a chunk
+        const uint16_t *row = source_row<CACHE>(a, n, live ? h : 0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = 8 * c + j;
             p[j] = live && e < rot ? bf16_lo(row[e < half ? e + half : e - half]) : 0.f;
         }
     }
+    // two at a time; each lane of the packed instructions rounds like the scalar one
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (8 * c + j < rot)
-            x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(p[j], sn[j]));
+    for (int j = 0; j < 8; j += 2) {
+        const float2 y = f2_split(add2(mul2(f2(x[j], x[j + 1]), f2(cs[j], cs[j + 1])),
+                                       mul2(f2(p[j], p[j + 1]), f2(sn[j], sn[j + 1]))));
+        if (8 * c + j < rot)  // rot is even
+            x[j] = y.x, x[j + 1] = y.y;
+    }
 }
 
 __device__ __forceinline__ void widen(const uint4 &r, float (&x)[8])
@@ -149,12 +166,86 @@ __device__ __forceinline__ uint32_t int8x4(const float *x)
     return w;
 }
 
-// LG lanes a row, R rows a lane.  CACHE: append (q rotated to q_out, k and v into the cache),
-// else plain rotation of q to q_out.
-template <int LG, int R, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
+// One row (16-byte chunk c of it in `raw`), rotated and written where it belongs.  All lanes of the
+// warp call it.
+template <int LG, bool CACHE>
+__device__ __forceinline__ void put_row(const RowsArgs &a, const uint4 &raw, int h, int n, int c,
+                                        int lane, bool turns, const float (&cs)[8], const float (&sn)[8],
+                                        const TokenPlace &place)
 {
-    constexpr int kGroups = 32 / LG;
+    const bool in_dim = 8 * c < a.dim, live = h < a.rows;
+    const int qh = a.q.heads, kvh = CACHE ? a.cache.heads : 0;
+    float x[8];
+    widen(raw, x);
+    // values are not rotated: a warp that has only those skips it
+    const bool turned = turns && live && (!CACHE || h < qh + kvh);
+    if (__any_sync(0xffffffffu, turned)) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            y[j] = x[j];
+        turn<LG, CACHE>(a, n, h, raw, live && in_dim, c, lane, cs, sn, y);
+        if (turned) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = y[j];
+        }
+        __syncwarp();  // q_out may be q: partners are read before any lane writes
+    }
+    if (!CACHE || h < qh) {
+        if (live && in_dim)
+            *reinterpret_cast<uint4 *>(a.q_out.data + n * a.q_out.token_stride + h * a.q_out.head_stride + 8 * c) =
+                narrow(x);
+    }
+    if constexpr (CACHE) {
+        const bool is_v = h >= qh + kvh;
+        const int hh = h - qh - (is_v ? kvh : 0);
+        const bool put = live && h >= qh && place.row >= 0;
+        const long long row = place.row + static_cast<long long>(hh) * a.cache.page_size;
+        if (a.cache.type == kBf16) {
+            if (put && in_dim)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_v ? a.cache.v : a.cache.k) + row * a.dim + 8 * c) =
+                    narrow(x);
+            return;
+        }
+        if (!__any_sync(0xffffffffu, put))  // queries only
+            return;
+        // magnitudes compare as integers, with infinities and NaN above every finite value
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = LG / 2; o > 0; o >>= 1)
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float top = a.cache.type == kE4m3 ? 448.f : 127.f;
+        const float mf = __uint_as_float(m);
+        const bool finite = m < 0x7F800000u, held = finite && mf >= kTiny;
+        const float inv = held ? __fdiv_rn(top, mf) : 0.f;
+        const float scale = held ? __fdiv_rn(mf, top) : finite ? 0.f : __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = held ? __fmul_rn(x[j], inv) : 0.f;
+        if (put && in_dim) {
+            uint2 w;
+            if (a.cache.type == kE4m3)
+                w = make_uint2(e4m3x4(x), e4m3x4(x + 4));
+            else
+                w = make_uint2(int8x4(x), int8x4(x + 4));
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.cache.v : a.cache.k) + row * a.dim + 8 * c) = w;
+            if (c == 0)
+                (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = scale;
+        }
+    }
+}
+
+// A warp's rows of one token: LG lanes a row, R rows a lane at a time, the next R on their way
+// while these are worked on.  CACHE: append (q rotated to q_out, k and v into the cache), else
+// plain rotation of q to q_out.
+template <int LG, int R, bool CACHE>
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsArgs a)
+{
+    constexpr int kGroups = 32 / LG, kStep = R * kGroups;
     const int lane = threadIdx.x & 31, c = lane & (LG - 1), grp = lane / LG;
     const int unit = blockIdx.x * kWarps + static_cast<int>(threadIdx.x >> 5);
     griddep_launch_dependents();
@@ -162,27 +253,19 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     const int n = unit / a.units_per_token;
     if (n >= a.N)
         return;
-    const int row0 = (unit - n * a.units_per_token) * (R * kGroups) + grp;
-    const int qh = a.q.heads;
-    const int kvh = CACHE ? a.cache.heads : 0;
-
-    // the rows' loads first: they do not wait for the lookups
-    const uint16_t *src[R];
-    uint4 raw[R];
-    const bool in_dim = 8 * c < a.dim;
+    const int first = (unit - n * a.units_per_token) * a.rows_per_unit;
+    const int last = min(first + a.rows_per_unit, a.rows);
+    uint4 raw[R], next[R];
+    auto load = [&](int h0, uint4(&to)[R]) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        int h = row0 + i * kGroups;
-        src[i] = nullptr;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (h < a.rows) {
-            const HeadRows &s = h < qh ? a.q : h < qh + kvh ? a.k : a.v;
-            h -= h < qh ? 0 : h < qh + kvh ? qh : qh + kvh;
-            src[i] = s.data + n * s.token_stride + h * s.head_stride;
-            if (in_dim)
-                raw[i] = *reinterpret_cast<const uint4 *>(src[i] + 8 * c);
+        for (int i = 0; i < R; ++i) {
+            const int h = h0 + grp + i * kGroups;
+            to[i] = make_uint4(0, 0, 0, 0);
+            if (h < last && 8 * c < a.dim)
+                to[i] = *reinterpret_cast<const uint4 *>(source_row<CACHE>(a, n, h) + 8 * c);
         }
-    }
+    };
+    load(first, raw);  // before the lookups, which it does not wait for
     TokenPlace place{0, -1};
     if constexpr (CACHE)
         place = token_place(a.cache, a.tokens, n, lane);
@@ -192,70 +275,16 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowsArgs a)
     const bool turns = a.rope.table != nullptr;
     if (turns)
         load_turn(a, place.pos, c, cs, sn);
-
+    for (int h0 = first; h0 < last; h0 += kStep) {
+        load(h0 + kStep, next);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int h = row0 + i * kGroups;
-        const bool live = h < a.rows;
-        float x[8];
-        widen(raw[i], x);
-        if (turns) {
-            float y[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[j] = x[j];
-            turn<LG>(a, src[i], raw[i], live && in_dim, c, lane, cs, sn, y);
-            if (!CACHE || h < qh + kvh) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = y[j];
-            }
-            __syncwarp();  // q_out may be q: partners are read before any lane writes
+        for (int i = 0; i < R; ++i) {
+            const int h = h0 + grp + i * kGroups;
+            put_row<LG, CACHE>(a, raw[i], h < last ? h : a.rows, n, c, lane, turns, cs, sn, place);
         }
-        if (!CACHE || h < qh) {
-            if (live && in_dim)
-                *reinterpret_cast<uint4 *>(a.q_out.data + n * a.q_out.token_stride + h * a.q_out.head_stride + 8 * c) =
-                    narrow(x);
-        }
-        if constexpr (CACHE) {
-            const bool is_v = h >= qh + kvh;
-            const int hh = h - qh - (is_v ? kvh : 0);
-            const bool put = live && h >= qh && place.row >= 0;
-            const long long row = place.row + static_cast<long long>(hh) * a.cache.page_size;
-            if (a.cache.type == kBf16) {
-                if (put && in_dim)
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_v ? a.cache.v : a.cache.k) + row * a.dim +
-                                               8 * c) = narrow(x);
-                continue;
-            }
-            // magnitudes compare as integers, with infinities and NaN above every finite value
-            uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                m = max(m, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-#pragma unroll
-            for (int o = LG / 2; o > 0; o >>= 1)
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float top = a.cache.type == kE4m3 ? 448.f : 127.f;
-            const float mf = __uint_as_float(m);
-            const bool finite = m < 0x7F800000u, held = finite && mf >= kTiny;
-            const float inv = held ? __fdiv_rn(top, mf) : 0.f;
-            const float scale = held ? __fdiv_rn(mf, top) : finite ? 0.f : __uint_as_float(0x7FC00000u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = held ? __fmul_rn(x[j], inv) : 0.f;
-            if (put && in_dim) {
-                uint2 w;
-                if (a.cache.type == kE4m3)
-                    w = make_uint2(e4m3x4(x), e4m3x4(x + 4));
-                else
-                    w = make_uint2(int8x4(x), int8x4(x + 4));
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? a.cache.v : a.cache.k) + row * a.dim + 8 * c) =
-                    w;
-                if (c == 0)
-                    (is_v ? a.cache.v_scale : a.cache.k_scale)[row] = scale;
-            }
-        }
+        for (int i = 0; i < R; ++i)
+            raw[i] = next[i];
     }
 }
 
@@ -372,10 +401,15 @@ __global__ void rope_table_kernel(const RopeScaling s, int max_pos, int rot, flo
 }
 
 template <int LG, int R, bool CACHE>
-cudaError_t launch_rows(RowsArgs a, cudaStream_t stream)
+cudaError_t launch_rows(RowsArgs a, bool few, cudaStream_t stream)
 {
-    const int per_warp = R * (32 / LG);
-    a.units_per_token = (a.rows + per_warp - 1) / per_warp;
+    // Few rows: each warp takes one step of them, so that the call spreads over the SMs; many: a warp
+    // takes all of a token's, and one lookup and one set of cosines and sines serve them.  The chain
+    // of loads before the first result is long, so warps count more than rows in flight a warp:
+    // 16384 tokens of 32 + 2 * 8 rows to e4m3, 4 rows a step at 16 warps an SM 103.7 us, 2 rows a step
+    // at 32 warps 95.7; a warp a step (one token's lookup every 4 or 8 rows) 216 and 174.
+    a.rows_per_unit = few ? R * (32 / LG) : a.rows;
+    a.units_per_token = (a.rows + a.rows_per_unit - 1) / a.rows_per_unit;
     const long long units = static_cast<long long>(a.N) * a.units_per_token;
     const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
     return launch_dependent(rows_kernel<LG, R, CACHE>, dim3(grid), dim3(kThreads), 0, stream, a);
@@ -387,12 +421,11 @@ cudaError_t launch_rows(RowsArgs a, cudaStream_t stream)
     const int rot = a.rope.rot;
     a.vec_table = rot % 8 == 0 && reinterpret_cast<uintptr_t>(a.rope.table) % 16 == 0;
     a.shuffle = !a.rope.interleaved && (rot / 2) % 8 == 0;
-    // few rows: one row a lane, so that the call spreads over the SMs; many: four, which share
-    // one lookup and one set of cosines and sines
-    const bool few = static_cast<long long>(a.N) * a.rows <= 16LL * device_sm_count() * kWarps;
+    const long long rows = static_cast<long long>(a.N) * a.rows;
+    const bool few = rows <= 16LL * device_sm_count() * kWarps, some = a.N <= 4LL * device_sm_count() * kWarps;
     if (a.dim > 128)
-        return few ? launch_rows<32, 1, CACHE>(a, stream) : launch_rows<32, 4, CACHE>(a, stream);
-    return few ? launch_rows<16, 1, CACHE>(a, stream) : launch_rows<16, 4, CACHE>(a, stream);
+        return few ? launch_rows<32, 1, CACHE>(a, true, stream) : launch_rows<32, 2, CACHE>(a, some, stream);
+    return few ? launch_rows<16, 1, CACHE>(a, true, stream) : launch_rows<16, 2, CACHE>(a, some, stream);
 }
 
 }  // namespace
@@ -447,13 +480,15 @@ cudaError_t launch_cache_read(const PagedCache &cache, const TokenBatch &tokens,
     a.k = k_out;
     a.v = v_out;
     a.rows = 2 * cache.heads;
-    const bool few = static_cast<long long>(tokens.N) * a.rows <= 16LL * device_sm_count() * kWarps;
-    const int per_warp = few ? 2 : 8;
-    a.units_per_token = (a.rows + per_warp - 1) / per_warp;
+    // rows a lane holds at once: more of them share a lookup, but the call must spread over the SMs
+    // (65536 tokens of 2 * 8 rows 73.7 us at 4, 70.3 at 8; 5,000 of 2 * 3 rows 5.1 and 6.1 us)
+    const long long rows = static_cast<long long>(tokens.N) * a.rows;
+    const int per_lane = rows <= 16LL * device_sm_count() * kWarps ? 1 : rows <= 256LL * device_sm_count() * kWarps ? 4 : 8;
+    a.units_per_token = (a.rows + 2 * per_lane - 1) / (2 * per_lane);
     const long long units = static_cast<long long>(tokens.N) * a.units_per_token;
     const dim3 grid(static_cast<unsigned>((units + kWarps - 1) / kWarps));
-    return few ? launch_dependent(read_kernel<1>, grid, dim3(kThreads), 0, stream, a)
-               : launch_dependent(read_kernel<4>, grid, dim3(kThreads), 0, stream, a);
+    const auto kernel = per_lane == 1 ? read_kernel<1> : per_lane == 4 ? read_kernel<4> : read_kernel<8>;
+    return launch_dependent(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace df2

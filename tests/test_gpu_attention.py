@@ -487,3 +487,41 @@ def test_no_tokens(at):
     assert at.dflash2_cache_read(cache, b.on_gpu(at))["k"].shape == (0, 2, 64)
     assert at.dflash2_paged_attention(empty, cache, b.on_gpu(at))["out"].shape == (0, 2, 64)
     assert at.dflash2_rope(empty, torch.empty(0, dtype=torch.int32, device="cuda"), make_table(4, 8)).shape == (0, 2, 64)
+
+
+# ---------------------------------------------------------------------------------------- all together
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+def test_draft_steps(at, kind):
+    """The example's layer: every step's attention equals the plain form over what the cache holds."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_step.py")
+    spec = importlib.util.spec_from_file_location("draft_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    B, T = 3, 8
+    step = example.DraftStep(B, T, cache_type=kind, max_len=64)
+    ids = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+    anchor = torch.tensor([5, 9, 77], dtype=torch.int32, device="cuda")
+    for n in range(3):
+        ids = step(ids, anchor)
+        anchor = ids[:, -1].contiguous()
+        held = T * (n + 1)
+        whole = at.TokenBatch(torch.arange(B + 1, dtype=torch.int32, device="cuda") * held, step.kv_len,
+                              step.tokens.page_table, tokens=B * held, max_new=held)
+        if kind == "bf16":
+            back = at.dflash2_cache_read(step.cache, whole)
+            k, v = (list(back[x].double().view(B, held, step.kv_heads, step.dim)) for x in ("k", "v"))
+        else:
+            p = torch.arange(held, device="cuda")
+            pages, slots = step.tokens.page_table[:, p // 16].long(), p % 16
+            k, v = ([getattr(step.cache, x).view(torch.uint8)[pages[b], :, slots].view(example.TYPES[kind]).double() *
+                     getattr(step.cache, x + "_scale")[pages[b], :, slots].double()[..., None] for b in range(B)]
+                    for x in ("k", "v"))
+        q = step.qkv[:, :step.q_heads]
+        want, mag, _ = attend(q, k, v, [held] * B, [T] * B, step.dim ** -0.5, False, 0)
+        assert ((step.out.double() - want).abs() <= attend_bound(want, mag)).all()
+        assert ids.shape == (B, T) and (ids >= 0).all() and (ids < 8192).all()
