@@ -36,7 +36,7 @@ class DraftStep:
 
         self.B, self.T, self.H, self.q_heads, self.kv_heads, self.dim, self.k = B, T, H, q_heads, kv_heads, dim, k
         self.embed, self.w_qkv = w(V, H, scale=1.0), w((q_heads + 2 * kv_heads) * dim, H)
-        self.w_out = w(H, q_heads * dim)
+        self.w_out, self.head = w(H, q_heads * dim), w(V, H)
         self.conv_base = torch.zeros(2, H, dtype=BF16, device="cuda")
         self.conv_base[0] = 1
         self.conv_dyn = torch.randn(B * T, 2, H // 16, device="cuda", generator=g) * 0.1
@@ -67,7 +67,7 @@ class DraftStep:
         self.append()
         self.out = self.attend()["out"]
         hidden = x + self.out.reshape(self.B * self.T, -1) @ self.w_out.t()
-        _, draft = df.dflash2_select(hidden, self.embed, self.W_sel, self.pred_cb, self.succ_cb, anchor, self.k, self.T,
+        _, draft = df.dflash2_select(hidden, self.head, self.W_sel, self.pred_cb, self.succ_cb, anchor, self.k, self.T,
                                      workspace=self.workspace)
         return draft
 

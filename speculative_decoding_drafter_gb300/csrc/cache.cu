@@ -16,9 +16,9 @@
 // and every pair's partner is in the lane itself or one shuffle away.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
-#include "f32x2.cuh"
 #include "internal.h"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -41,7 +41,7 @@ struct RowsArgs {
     int N, dim;
     float sine_sign;
     int rows;            // rows of a token: q heads, then cache heads of k, then of v
-    int rows_per_unit, units_per_token;
+    int units_per_token;
     int vec_table;  // cosines and sines in 16-byte loads
     int shuffle;    // half layout: partners are whole chunks of other lanes
 };
@@ -128,14 +128,12 @@ __device__ __forceinline__ void turn(const RowsArgs &a, int n, int h, const uint
             p[j] = live && e < rot ? bf16_lo(row[e < half ? e + half : e - half]) : 0.f;
         }
     }
-    // two at a time; each lane of the packed instructions rounds like the scalar one
+    // one by one: a packed product and a packed sum come out as one rounding (measured), and the codes
+    // of an 8-bit cache are to be those of the formula's separate operations
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-        const float2 y = f2_split(add2(mul2(f2(x[j], x[j + 1]), f2(cs[j], cs[j + 1])),
-                                       mul2(f2(p[j], p[j + 1]), f2(sn[j], sn[j + 1]))));
-        if (8 * c + j < rot)  // rot is even
-            x[j] = y.x, x[j + 1] = y.y;
-    }
+    for (int j = 0; j < 8; ++j)
+        if (8 * c + j < rot)
+            x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(p[j], sn[j]));
 }
 
 __device__ __forceinline__ void widen(const uint4 &r, float (&x)[8])
@@ -239,13 +237,13 @@ __device__ __forceinline__ void put_row(const RowsArgs &a, const uint4 &raw, int
     }
 }
 
-// A warp's rows of one token: LG lanes a row, R rows a lane at a time, the next R on their way
-// while these are worked on.  CACHE: append (q rotated to q_out, k and v into the cache), else
-// plain rotation of q to q_out.
+// LG lanes a row, R rows a lane at a time.  CACHE: append (q rotated to q_out, k and v into the
+// cache), else plain rotation of q to q_out.
+// One step (few tokens): a warp takes R * 32 / LG rows of a token.
 template <int LG, int R, bool CACHE>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsArgs a)
 {
-    constexpr int kGroups = 32 / LG, kStep = R * kGroups;
+    constexpr int kGroups = 32 / LG;
     const int lane = threadIdx.x & 31, c = lane & (LG - 1), grp = lane / LG;
     const int unit = blockIdx.x * kWarps + static_cast<int>(threadIdx.x >> 5);
     griddep_launch_dependents();
@@ -253,19 +251,14 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsArgs a)
     const int n = unit / a.units_per_token;
     if (n >= a.N)
         return;
-    const int first = (unit - n * a.units_per_token) * a.rows_per_unit;
-    const int last = min(first + a.rows_per_unit, a.rows);
-    uint4 raw[R], next[R];
-    auto load = [&](int h0, uint4(&to)[R]) {
+    const int first = (unit - n * a.units_per_token) * R * kGroups + grp;
+    uint4 raw[R];  // loaded before the lookups, which they do not wait for
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int h = h0 + grp + i * kGroups;
-            to[i] = make_uint4(0, 0, 0, 0);
-            if (h < last && 8 * c < a.dim)
-                to[i] = *reinterpret_cast<const uint4 *>(source_row<CACHE>(a, n, h) + 8 * c);
-        }
-    };
-    load(first, raw);  // before the lookups, which it does not wait for
+    for (int i = 0; i < R; ++i) {
+        const int h = first + i * kGroups;
+        raw[i] = h < a.rows && 8 * c < a.dim ? *reinterpret_cast<const uint4 *>(source_row<CACHE>(a, n, h) + 8 * c)
+                                             : make_uint4(0, 0, 0, 0);
+    }
     TokenPlace place{0, -1};
     if constexpr (CACHE)
         place = token_place(a.cache, a.tokens, n, lane);
@@ -275,16 +268,61 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsArgs a)
     const bool turns = a.rope.table != nullptr;
     if (turns)
         load_turn(a, place.pos, c, cs, sn);
-    for (int h0 = first; h0 < last; h0 += kStep) {
-        load(h0 + kStep, next);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        put_row<LG, CACHE>(a, raw[i], first + i * kGroups, n, c, lane, turns, cs, sn, place);
+}
+
+// Many tokens: a warp takes all rows of `run` tokens in a row, the next R rows a lane on their way
+// while R are worked on.  The tokens' places are looked up at once, a lane each, and the next
+// token's cosines and sines are asked for when only values, which do not turn, are left of this one.
+template <int LG, int R, bool CACHE>
+__global__ void __launch_bounds__(kThreads, 4) rows_run_kernel(const RowsArgs a, int run)
+{
+    constexpr int kGroups = 32 / LG, kStep = R * kGroups;
+    const int lane = threadIdx.x & 31, c = lane & (LG - 1), grp = lane / LG;
+    const int n0 = (blockIdx.x * kWarps + static_cast<int>(threadIdx.x >> 5)) * run;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (n0 >= a.N)
+        return;
+    const int count = min(run, a.N - n0);
+    uint4 raw[R], next[R];
+    auto load = [&](int n, int h0, uint4(&to)[R]) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int h = h0 + grp + i * kGroups;
-            put_row<LG, CACHE>(a, raw[i], h < last ? h : a.rows, n, c, lane, turns, cs, sn, place);
+            to[i] = h < a.rows && 8 * c < a.dim ? *reinterpret_cast<const uint4 *>(source_row<CACHE>(a, n, h) + 8 * c)
+                                                : make_uint4(0, 0, 0, 0);
         }
+    };
+    load(n0, 0, raw);
+    TokenPlace mine{0, -1};  // of token n0 + lane
+    if constexpr (CACHE)
+        mine = lane_token_place(a.cache, a.tokens, n0, count, lane);
+    else
+        mine.pos = lane < count ? __ldg(a.positions + n0 + lane) : 0;
+    float cs[8], sn[8];
+    const bool turns = a.rope.table != nullptr;
+    const int turned = CACHE ? a.q.heads + a.cache.heads : a.rows;  // rows that turn
+    if (turns)
+        load_turn(a, __shfl_sync(0xffffffffu, mine.pos, 0), c, cs, sn);
+    for (int t = 0; t < count; ++t) {
+        const int n = n0 + t;
+        const TokenPlace place{0, __shfl_sync(0xffffffffu, mine.row, t)};
+        const int next_pos = __shfl_sync(0xffffffffu, mine.pos, min(t + 1, count - 1));
+        for (int h0 = 0; h0 < a.rows; h0 += kStep) {
+            const bool more = h0 + kStep < a.rows;
+            load(more ? n : min(n + 1, n0 + count - 1), more ? h0 + kStep : 0, next);
 #pragma unroll
-        for (int i = 0; i < R; ++i)
-            raw[i] = next[i];
+            for (int i = 0; i < R; ++i)
+                put_row<LG, CACHE>(a, raw[i], h0 + grp + i * kGroups, n, c, lane, turns, cs, sn, place);
+            if (turns && h0 < turned && h0 + kStep >= turned)
+                load_turn(a, next_pos, c, cs, sn);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                raw[i] = next[i];
+        }
     }
 }
 
@@ -401,31 +439,41 @@ __global__ void rope_table_kernel(const RopeScaling s, int max_pos, int rot, flo
 }
 
 template <int LG, int R, bool CACHE>
-cudaError_t launch_rows(RowsArgs a, bool few, cudaStream_t stream)
+cudaError_t launch_step(RowsArgs a, cudaStream_t stream)
 {
-    // Few rows: each warp takes one step of them, so that the call spreads over the SMs; many: a warp
-    // takes all of a token's, and one lookup and one set of cosines and sines serve them.  The chain
-    // of loads before the first result is long, so warps count more than rows in flight a warp:
-    // 16384 tokens of 32 + 2 * 8 rows to e4m3, 4 rows a step at 16 warps an SM 103.7 us, 2 rows a step
-    // at 32 warps 95.7; a warp a step (one token's lookup every 4 or 8 rows) 216 and 174.
-    a.rows_per_unit = few ? R * (32 / LG) : a.rows;
-    a.units_per_token = (a.rows + a.rows_per_unit - 1) / a.rows_per_unit;
+    constexpr int kPerWarp = R * (32 / LG);
+    a.units_per_token = (a.rows + kPerWarp - 1) / kPerWarp;
     const long long units = static_cast<long long>(a.N) * a.units_per_token;
     const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
     return launch_dependent(rows_kernel<LG, R, CACHE>, dim3(grid), dim3(kThreads), 0, stream, a);
 }
 
-template <bool CACHE>
+template <int LG, bool CACHE>
 cudaError_t launch_rows(RowsArgs a, cudaStream_t stream)
 {
     const int rot = a.rope.rot;
     a.vec_table = rot % 8 == 0 && reinterpret_cast<uintptr_t>(a.rope.table) % 16 == 0;
     a.shuffle = !a.rope.interleaved && (rot / 2) % 8 == 0;
-    const long long rows = static_cast<long long>(a.N) * a.rows;
-    const bool few = rows <= 16LL * device_sm_count() * kWarps, some = a.N <= 4LL * device_sm_count() * kWarps;
-    if (a.dim > 128)
-        return few ? launch_rows<32, 1, CACHE>(a, true, stream) : launch_rows<32, 2, CACHE>(a, some, stream);
-    return few ? launch_rows<16, 1, CACHE>(a, true, stream) : launch_rows<16, 2, CACHE>(a, some, stream);
+    // A warp's life is a chain of loads (the sequence, its length, the page, the cosines) whatever it
+    // carries, so it should carry much while enough warps are left: a row a lane while that fits 32
+    // warps an SM, then four, then whole tokens with the next rows on their way, and several tokens
+    // where they have few rows.  Measured on GB300, four rows a lane against whole tokens: 2048
+    // tokens of 48 rows to int8 19.1 and 28.4 us, 8195 of 32 rows turned 29.8 and 28.8, 16384 of 48
+    // to e4m3 107.6 and 88.9; one token a warp against twenty: 100,000 of 4 rows 74 and 54 us.
+    const long long rows = static_cast<long long>(a.N) * a.rows, wave = 32LL * device_sm_count();
+    if (rows <= wave * (32 / LG))
+        return launch_step<LG, 1, CACHE>(a, stream);
+    if (rows <= 16 * wave * (32 / LG))
+        return launch_step<LG, 4, CACHE>(a, stream);
+    const int run = a.rows >= 32 ? 1 : static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(32, 96 / a.rows), a.N / wave)));
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.N) + run * kWarps - 1) / (run * kWarps));
+    return launch_dependent(rows_run_kernel<LG, 2, CACHE>, dim3(grid), dim3(kThreads), 0, stream, a, run);
+}
+
+template <bool CACHE>
+cudaError_t launch_rows(const RowsArgs &a, cudaStream_t stream)
+{
+    return a.dim > 128 ? launch_rows<32, CACHE>(a, stream) : launch_rows<16, CACHE>(a, stream);
 }
 
 }  // namespace

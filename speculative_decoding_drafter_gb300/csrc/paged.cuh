@@ -30,9 +30,8 @@ struct TokenPlace {
     long long row;
 };
 
-__device__ __forceinline__ TokenPlace token_place(const PagedCache &c, const TokenBatch &t, int n, int lane)
+__device__ __forceinline__ TokenPlace place_in(const PagedCache &c, const TokenBatch &t, int b, int n)
 {
-    const int b = warp_sequence_of(t.token_start, t.B, n, lane);
     const int pos = __ldg(t.kv_len + b) - __ldg(t.token_start + b + 1) + n;
     TokenPlace p{pos, -1};
     if (pos >= 0 && static_cast<long long>(pos) < static_cast<long long>(t.max_pages) * c.page_size) {
@@ -41,6 +40,24 @@ __device__ __forceinline__ TokenPlace token_place(const PagedCache &c, const Tok
             p.row = static_cast<long long>(page) * c.heads * c.page_size + pos % c.page_size;
     }
     return p;
+}
+
+// Token n's place; one warp.
+__device__ __forceinline__ TokenPlace token_place(const PagedCache &c, const TokenBatch &t, int n, int lane)
+{
+    return place_in(c, t, warp_sequence_of(t.token_start, t.B, n, lane), n);
+}
+
+// The places of the tokens n0 .. n0 + count - 1 (count <= 32), a lane each; one warp.
+__device__ __forceinline__ TokenPlace lane_token_place(const PagedCache &c, const TokenBatch &t, int n0, int count,
+                                                       int lane)
+{
+    int b = warp_sequence_of(t.token_start, t.B, n0, lane);
+    if (lane >= count)
+        return TokenPlace{0, -1};
+    while (b + 1 < t.B && __ldg(t.token_start + b + 1) <= n0 + lane)
+        ++b;
+    return place_in(c, t, b, n0 + lane);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
