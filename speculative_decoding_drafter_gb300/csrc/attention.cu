@@ -7,25 +7,45 @@
 // in the 16-bit probabilities) the old m is kept, so o is seldom touched.
 //
 // A work item is a sequence, a cache head and a run of its new tokens: the query heads that share
-// the cache head are rows of the same tile (token major), 128 rows a tile, one or two tiles.
-// Each CTA (one per SM) takes an equal share of all (item, key tile) pairs in order; an item that
-// crosses a border is finished by the combine kernel from partial (o, m, l).
+// the cache head are rows of the same tile (token major), 128 rows a tile, one or two tiles (two when
+// a sequence may have more rows than one holds: they share every K and V tile read).  Each CTA (one
+// per SM) takes an equal share of all (item, key tile) pairs in order, so lengths may differ at will
+// and few items still fill the GPU; an item that crosses a border is finished by the combine kernel
+// from partial (o, m, l), pieces in order, so results do not depend on timing.
 //
-// Roles of a CTA: warp 0 loads K and V tiles by TMA, a box per run of a page; one thread of warp 1
-// issues the MMAs; a warpgroup per row tile does the softmax, a thread per row, S read from and P
-// written back to tensor memory; with an 8-bit cache two more warpgroups
-// widen the codes to f16, one K's and one V's.
-//   S = Q K^T   both K-major from shared memory          D[128 x 128] in TMEM
+// Roles of a CTA:
+//   warp 0     walks the work and hands segments to the others; loads K tiles by TMA, a box per run of
+//              rows of a page (gcd(page_size, 128) of them), pages looked up 32 at a time
+//   warp 3     loads V tiles;   warp 2   (8-bit cache) prepares the tile's scales
+//   warp 1     one elected lane issues the MMAs
+//   a warpgroup per row tile: softmax, a thread per row, S read from and P written back to TMEM
+//   two warpgroups (8-bit cache): widen codes to f16 in shared memory, one K's and one V's
+//   S = Q K^T   K from shared memory as it lies, Q from TMEM (one row tile) or shared memory (two)
 //   O += P V    P from TMEM over S, V as it lies (its rows are the K dimension: MN-major B)
+// One row tile: two S take turns, so the next S is ready when a softmax ends.  Two row tiles: one S
+// each (TMEM is full), and the products of one run under the softmax of the other.
+//
 // Few rows (a draft block of one cache head is often 8 to 64 of them) leave most of a 128-row tile
-// empty, and a thread that walks 128 scores is then the longest step of a tile.  The tile holds
-// such rows FOLD = 2 or 4 times over instead: every copy takes 128 / FOLD of a tile's keys (its P
-// is zero elsewhere), with its own m and l, and the copies are added up at the end of the item.
+// empty, and a thread that walks 128 scores is then the longest step of a tile.  With an 8-bit cache
+// the tile holds such rows FOLD = 2 or 4 times over: every copy takes 128 / FOLD of a tile's keys (its
+// P is zero elsewhere), with its own m and l, and the copies are added up at the end of the item.
 // 8-bit caches: codes are exact in f16, so K's scale multiplies the score, and V's goes into the
 // exponent: x'_j = x_j + log2(vs_j), P'_j = 2^(x'_j - m'), o = sum P'_j code_j, l = sum P'_j / vs_j,
 // which keeps P' in f16's range whatever the values' size.  Queries go to f16 by a power of two per
 // row that brings the row's largest magnitude to 2^14..2^15 (smaller parts lose bits only below
-// 2^-24 of it).  With a bf16 cache everything stays bf16; P is rounded once, to bf16 or f16.
+// 2^-24 of it).  With a bf16 cache everything stays bf16; P is rounded once, to bf16 or f16, as the
+// MMA's operand; scores, sums and o are float32.
+//
+// What bounds it, and measured on one GB300 (copy 6768 GB/s, cuBLAS bf16 1957 TFLOP/s burst):
+//   32 sequences x 16 tokens, up to 8192 keys, 32 / 8 heads of 128, bf16: HBM; 132 us, 5.9 TB/s
+//     (the kernel alone 124 us and 1.01 times the algorithmic bytes; the rest is the combine kernel)
+//   32 x 8 tokens, up to 16384 keys, e4m3: shared memory, which the codes cross three times (TMA in,
+//     widening, MMA); 178 us, 4.5 TB/s
+//   one sequence, 2048 tokens over 18432 keys, bf16: the chain of a tile's softmax and products;
+//     383 us cold, 1.52 PFLOP/s, 400 to 420 back to back under the power cap
+//   one token over 777 keys: a chain of latencies (lengths, pages, tile, softmax, combine); 9.7 us
+// The code of all roles has to fit the instruction cache: with the walk in every role and loops
+// unrolled (11,200 instructions) warps waited for instructions and the e4m3 case took 330 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

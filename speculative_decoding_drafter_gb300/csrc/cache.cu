@@ -465,7 +465,7 @@ cudaError_t launch_rows(RowsArgs a, cudaStream_t stream)
         return launch_step<LG, 1, CACHE>(a, stream);
     if (rows <= 16 * wave * (32 / LG))
         return launch_step<LG, 4, CACHE>(a, stream);
-    const int run = a.rows >= 32 ? 1 : static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(32, 96 / a.rows), a.N / wave)));
+    const int run = a.rows >= 32 ? 1 : static_cast<int>(std::max<long long>(1, std::min<long long>(std::min(32, 96 / a.rows), (a.N + wave - 1) / wave)));
     const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.N) + run * kWarps - 1) / (run * kWarps));
     return launch_dependent(rows_run_kernel<LG, 2, CACHE>, dim3(grid), dim3(kThreads), 0, stream, a, run);
 }
