@@ -466,7 +466,10 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const uint32_t bar0 = sbase + lay.bars;
     // A barrier's phases are told apart by parity, so whoever waits on one must wait for every phase
     // of it.  The slots of a ring of odd size hold a K and a V in turn, which different warps load and
-    // widen: each has barriers of its own (next_kv: what the slot becomes free for).
+    // widen: each has barriers of its own (next_kv: what the slot becomes free for).  Where a phase is
+    // skipped, the one before must be known to be over: pv_done has a barrier for each S, not each row
+    // tile, because with one row tile an S that is ready says that the products two tiles back are in,
+    // not those of the last tile, and after a late V a wait on one barrier let go two phases early.
     auto ring_full = [&](int s, int kv) { return bar0 + 8u * (s + (kQuant ? kv * MAX_RING : 0)); };
     auto ring_empty = [&](int s, int next_kv) { return bar0 + 8u * (MAX_RING * (2 + next_kv) + s); };
     auto wide_full = [&](int s) { return bar0 + 8u * (4 * MAX_RING + s); };
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < BN / 16; ++kk)
                         umma_f16_tmem_a(d, p + kk * 8, desc_at(v + kk * (2048 >> 4), v_hi), idesc_pv, kk > 0 ? 1u : acc);
-                    umma_commit(pv_done(s));
+                    umma_commit(pv_done(sbuf));
                 }
                 __syncwarp();
             };
@@ -1033,6 +1036,12 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             return met;
         };
 
+        // waits for the products of tile cnt - 1
+        auto products_in = [&]() {
+            const int t = cnt - 1;
+            return QT == 2 ? warp_wait(pv_done(s), t & 1, abort_flag) : warp_wait(pv_done(t & 1), (t >> 1) & 1, abort_flag);
+        };
+
         // Segment n after segment n; before the first there is only its queries to load.
         bool more = true;
         for (int n = -1; more; ++n) {
@@ -1149,7 +1158,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         const bool move = live && rise > LAZY;
                         if (j > 0 && __any_sync(0xffffffffu, move)) {
                             // the products so far must be in before they are scaled
-                            ok = warp_wait(pv_done(s), (cnt - 1) & 1, abort_flag);
+                            ok = products_in();
                             if (!ok)
                                 break;
                             tc_fence_after();
@@ -1274,7 +1283,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             const long long part = static_cast<long long>(g.slot) * (QT * BM) + s * BM + trow;
             uint16_t *dst = a.out.data + static_cast<long long>(tok) * a.out.token_stride +
                             static_cast<long long>(head) * a.out.head_stride;
-            ok = warp_wait(pv_done(s), (cnt - 1) & 1, abort_flag);
+            ok = products_in();
             if (!ok)
                 break;
             tc_fence_after();

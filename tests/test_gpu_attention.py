@@ -451,6 +451,31 @@ def test_attention_long(at, dtype, new):
     assert ((got["lse"].double() - lse).abs() <= 2.0 ** -14 * (1 + lse.abs())).all()
 
 
+@TYPES
+@pytest.mark.parametrize("new", [1, 16, 40])
+def test_attention_beside_memory_traffic(at, dtype, new):
+    """Tiles that arrive late, one by one and at random: the products of every tile are in the result all the same."""
+    lens = [8192 - 157 * ((11 * i) % 32) for i in range(32)]
+    b = Batch(lens, [new] * 32, 64)
+    cache, k, v = filled(at, b, 4, 128, dtype, 8)
+    q = randn(gen(9), 32 * new, 16, 128).to(BF16)
+    want, mag, lse = attend(q, k, v, b.lens, b.news, 128 ** -0.5, True, 0)
+    batch = b.on_gpu(at)
+    ws = at.AttentionWorkspace(cache, batch, 16)
+    noise, side = torch.empty(1 << 28, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    runs = []
+    for _ in range(100):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(4):
+                noise.add_(1)
+        runs.append(at.dflash2_paged_attention(q, cache, batch, workspace=ws))
+        torch.cuda.current_stream().wait_stream(side)
+    assert ((runs[0]["out"].double() - want).abs() <= attend_bound(want, mag)).all()
+    assert ((runs[0]["lse"].double() - lse).abs() <= 2.0 ** -14 * (1 + lse.abs())).all()
+    assert all(torch.equal(r["out"], runs[0]["out"]) and torch.equal(r["lse"], runs[0]["lse"]) for r in runs[1:])
+
+
 def test_attention_many_sequences(at):
     """More sequences than lanes, SMs and probes of one lookup step, several of them empty."""
     lens = [(37 * i) % 211 for i in range(600)]
