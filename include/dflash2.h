@@ -348,7 +348,8 @@ DF2_API df2_status dflash2_rope(const df2_rope *rope, int32_t N, int32_t dim, co
 typedef enum df2_cache_type { DF2_CACHE_BF16 = 0, DF2_CACHE_E4M3 = 1, DF2_CACHE_INT8 = 2 } df2_cache_type;
 
 /* One layer's paged cache: k and v [pages, heads, page_size, dim] of the type, and for the 8-bit
- * types k_scale and v_scale float [pages, heads, page_size] (NULL for bf16), all 16-byte aligned.  A row (one token, one head) is held as codes times its scale:
+ * types k_scale and v_scale float [pages, heads, page_size] (NULL for bf16), all 16-byte aligned.
+ * A row (one token, one head) is held as codes times its scale:
  *   m = max |row|,  scale = m / M,  code = round(row * (M / m)),  M = 448 (e4m3) or 127 (int8),
  * each operation in float32, codes rounded to nearest even.  A row with m < 1e-30 is held as
  * zeros; one that is not finite gets a NaN scale and reads back as NaN throughout.
