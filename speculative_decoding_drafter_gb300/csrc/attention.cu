@@ -40,7 +40,7 @@
 //   32 sequences x 16 tokens, up to 8192 keys, 32 / 8 heads of 128, bf16: HBM; 132 us, 5.9 TB/s
 //     (the kernel alone 124 us and 1.01 times the algorithmic bytes; the rest is the combine kernel)
 //   32 x 8 tokens, up to 16384 keys, e4m3: shared memory, which the codes cross three times (TMA in,
-//     widening, MMA); 170 to 178 us, 4.5 to 4.7 TB/s
+//     widening, MMA); 170 to 179 us, 4.4 to 4.7 TB/s
 //   one sequence, 2048 tokens over 18432 keys, bf16: the chain of a tile's softmax and products;
 //     383 us cold, 1.52 PFLOP/s, 397 to 425 back to back under the power cap
 //   one token over 777 keys: a chain of latencies (lengths, pages, tile, softmax, combine); 9.7 us
