@@ -590,143 +590,143 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             mbar_arrive(seg_empty(n % SEGMENTS));
     };
 
-    if (warp == 0 || warp == 3) {
-        // ---------------------------------------------------------------- TMA producers: K, V
-        // Warp 0 also walks.  One lane issues with warp-uniform operands, box after box: lanes that
-        // issue their own boxes are taken one by one anyhow, at several times the cost.
+    if (warp < 4) {
+        // One place for the whole warpgroup: setmaxnreg wants all its warps at the same instruction, and
+        // the softmax warps' wait for what it gives back has no limit.
         if constexpr (Shape<QT, TYPE>::kSplitRegs)
             reg_dec<Shape<QT, TYPE>::kControlRegs>();
-        const int kv = warp == 0 ? 0 : 1;
-        const CUtensorMap *map = kv ? &map_v : &map_k;
-        long long units = 0;
-        if (kv == 0) {
-            int sum = 0;
-            if (lane == 0)
-                prefix[0] = 0;
-            for (int b0 = 0; b0 < B; b0 += 32) {
-                int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, t, o);
-                    t += lane >= o ? x : 0;
-                }
-                t += sum;
-                if (b0 + lane < B)
-                    prefix[b0 + lane + 1] = t;
-                sum = __shfl_sync(0xffffffffu, t, 31);
-            }
-            __syncwarp();
-            units = static_cast<long long>(sum) * a.cache.heads;
-        }
-        const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(units, 1ll)));
-        const Shares shares(units, grid);
-        Walk walk;
-        if (kv == 0 && cta < grid && units > 0)
-            walk.begin(a, near, prefix, shares, cta);
-        else
-            walk.u = walk.u_end = 0;
-        const int boxes = BN / a.box, per_batch = 32 / boxes;  // boxes of a tile, tiles of a batch of 32
-        const int ps = a.cache.page_size, dim = a.cache.dim;
-        const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
-        RingSlot rs{kv, 0};
-        int tcnt = 0;  // tiles begun
-        bool ok = true;
-        for (int n = 0; ok; ++n) {
-            const Segment &g = segs[n % SEGMENTS];
+        if (warp == 0 || warp == 3) {
+            // ---------------------------------------------------------------- TMA producers: K, V
+            // Warp 0 also walks.  One lane issues with warp-uniform operands, box after box: lanes that
+            // issue their own boxes are taken one by one anyhow, at several times the cost.
+            const int kv = warp == 0 ? 0 : 1;
+            const CUtensorMap *map = kv ? &map_v : &map_k;
+            long long units = 0;
             if (kv == 0) {
-                if (n >= SEGMENTS)
-                    ok = warp_wait(seg_empty(n % SEGMENTS), (n / SEGMENTS - 1) & 1, abort_flag);
-                if (!ok)
-                    break;
-                Segment next;
-                walk.next(a, cta, shares, next);
-                if (lane == 0) {
-                    segs[n % SEGMENTS] = next;
-                    mbar_arrive(seg_full(n % SEGMENTS));
-                }
-                __syncwarp();
-            } else {
-                ok = seg_wait(n);
-            }
-            const int tiles = g.tiles, kvh = g.kvh;
-            if (!ok || tiles == 0)
-                break;
-            const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
-            const int tok0 = g.tile * BN, lo = g.item.lo, hi = g.item.hi;
-            // 32 boxes' pages at a time, a lane each, the next 32 on their way: a load waits hundreds of
-            // cycles, too long to be met at every tile
-            auto pages_at = [&](int j) {
-                const int tok = tok0 + j * BN + lane * a.box;
-                const bool need = tok < hi && tok + a.box > lo;
-                return need ? min(max(__ldg(pt + page_of_token(a, tok)), 0), a.cache.pages - 1) : -1;
-            };
-            int batch = pages_at(0), next_batch = pages_at(per_batch), at = 0;
-            uint32_t needed = __ballot_sync(0xffffffffu, batch >= 0);
-            for (int j = 0; j < tiles; ++j) {
-                if (at == 32) {
-                    at = 0;
-                    batch = next_batch;
-                    needed = __ballot_sync(0xffffffffu, batch >= 0);
-                    next_batch = pages_at(j + per_batch);
-                }
-                const int tok = tok0 + j * BN;
-                const int here = __popc(needed >> at & ((1u << boxes) - 1u));
-                const int turn = rs.turn(a.ring, kv);
-                if (turn >= 0)
-                    ok = warp_wait(ring_empty(rs.slot, kv), turn & 1, abort_flag);
-                if (!ok)
-                    break;
-                const uint32_t full = ring_full(rs.slot, kv);
-                if (elect_one())
-                    mbar_arrive_expect_tx(full, here * box_bytes);
-                __syncwarp();
-                uint32_t dst = sbase + lay.ring + rs.slot * lay.ring_stage;
-                int in_page = tok - page_of_token(a, tok) * ps;
-#pragma unroll 1
-                for (int i = 0; i < boxes; i += 4) {
-                    int page[4], x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        page[k] = __shfl_sync(0xffffffffu, batch, (at + i + k) & 31);
-                        page[k] = i + k < boxes ? page[k] : -1;
-                        x[k] = in_page;
-                        in_page += a.box;
-                        in_page = in_page == ps ? 0 : in_page;
+                int sum = 0;
+                if (lane == 0)
+                    prefix[0] = 0;
+                for (int b0 = 0; b0 < B; b0 += 32) {
+                    int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int x = __shfl_up_sync(0xffffffffu, t, o);
+                        t += lane >= o ? x : 0;
                     }
-                    if (elect_one()) {
-#pragma unroll
+                    t += sum;
+                    if (b0 + lane < B)
+                        prefix[b0 + lane + 1] = t;
+                    sum = __shfl_sync(0xffffffffu, t, 31);
+                }
+                __syncwarp();
+                units = static_cast<long long>(sum) * a.cache.heads;
+            }
+            const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(units, 1ll)));
+            const Shares shares(units, grid);
+            Walk walk;
+            if (kv == 0 && cta < grid && units > 0)
+                walk.begin(a, near, prefix, shares, cta);
+            else
+                walk.u = walk.u_end = 0;
+            const int boxes = BN / a.box, per_batch = 32 / boxes;  // boxes of a tile, tiles of a batch of 32
+            const int ps = a.cache.page_size, dim = a.cache.dim;
+            const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
+            RingSlot rs{kv, 0};
+            int tcnt = 0;  // tiles begun
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                const Segment &g = segs[n % SEGMENTS];
+                if (kv == 0) {
+                    if (n >= SEGMENTS)
+                        ok = warp_wait(seg_empty(n % SEGMENTS), (n / SEGMENTS - 1) & 1, abort_flag);
+                    if (!ok)
+                        break;
+                    Segment next;
+                    walk.next(a, cta, shares, next);
+                    if (lane == 0) {
+                        segs[n % SEGMENTS] = next;
+                        mbar_arrive(seg_full(n % SEGMENTS));
+                    }
+                    __syncwarp();
+                } else {
+                    ok = seg_wait(n);
+                }
+                const int tiles = g.tiles, kvh = g.kvh;
+                if (!ok || tiles == 0)
+                    break;
+                const int32_t *pt = a.tokens.page_table + static_cast<long long>(g.b) * a.tokens.max_pages;
+                const int tok0 = g.tile * BN, lo = g.item.lo, hi = g.item.hi;
+                // 32 boxes' pages at a time, a lane each, the next 32 on their way: a load waits hundreds of
+                // cycles, too long to be met at every tile
+                auto pages_at = [&](int j) {
+                    const int tok = tok0 + j * BN + lane * a.box;
+                    const bool need = tok < hi && tok + a.box > lo;
+                    return need ? min(max(__ldg(pt + page_of_token(a, tok)), 0), a.cache.pages - 1) : -1;
+                };
+                int batch = pages_at(0), next_batch = pages_at(per_batch), at = 0;
+                uint32_t needed = __ballot_sync(0xffffffffu, batch >= 0);
+                for (int j = 0; j < tiles; ++j) {
+                    if (at == 32) {
+                        at = 0;
+                        batch = next_batch;
+                        needed = __ballot_sync(0xffffffffu, batch >= 0);
+                        next_batch = pages_at(j + per_batch);
+                    }
+                    const int tok = tok0 + j * BN;
+                    const int here = __popc(needed >> at & ((1u << boxes) - 1u));
+                    const int turn = rs.turn(a.ring, kv);
+                    if (turn >= 0)
+                        ok = warp_wait(ring_empty(rs.slot, kv), turn & 1, abort_flag);
+                    if (!ok)
+                        break;
+                    const uint32_t full = ring_full(rs.slot, kv);
+                    if (elect_one())
+                        mbar_arrive_expect_tx(full, here * box_bytes);
+                    __syncwarp();
+                    uint32_t dst = sbase + lay.ring + rs.slot * lay.ring_stage;
+                    int in_page = tok - page_of_token(a, tok) * ps;
+    #pragma unroll 1
+                    for (int i = 0; i < boxes; i += 4) {
+                        int page[4], x[4];
+    #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if (page[k] >= 0) {
-                                const uint32_t to = dst + k * a.box * (kQuant ? dim : 128);
-                                if constexpr (kQuant) {
-                                    tma_load_4d(to, map, full, 0, x[k], kvh, page[k]);
-                                } else {
-#pragma unroll
-                                    for (int h = 0; h < kHalves; ++h)
-                                        tma_load_4d(to + h * HALF_BYTES, map, full, h * 64, x[k], kvh, page[k]);
+                            page[k] = __shfl_sync(0xffffffffu, batch, (at + i + k) & 31);
+                            page[k] = i + k < boxes ? page[k] : -1;
+                            x[k] = in_page;
+                            in_page += a.box;
+                            in_page = in_page == ps ? 0 : in_page;
+                        }
+                        if (elect_one()) {
+    #pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (page[k] >= 0) {
+                                    const uint32_t to = dst + k * a.box * (kQuant ? dim : 128);
+                                    if constexpr (kQuant) {
+                                        tma_load_4d(to, map, full, 0, x[k], kvh, page[k]);
+                                    } else {
+    #pragma unroll
+                                        for (int h = 0; h < kHalves; ++h)
+                                            tma_load_4d(to + h * HALF_BYTES, map, full, h * 64, x[k], kvh, page[k]);
+                                    }
                                 }
                             }
                         }
+                        __syncwarp();
+                        dst += 4 * a.box * (kQuant ? dim : 128);
                     }
-                    __syncwarp();
-                    dst += 4 * a.box * (kQuant ? dim : 128);
+                    at += boxes;
+                    rs.step(a.ring);
+                    ++tcnt;
                 }
-                at += boxes;
-                rs.step(a.ring);
-                ++tcnt;
+                if (ok && kv == 1)
+                    seg_done(n);
             }
-            if (ok && kv == 1)
-                seg_done(n);
-        }
-        if (!ok) {  // let the copies already issued land before the CTA leaves
-            for (int n = max(tcnt - a.ring, 0); n < tcnt; ++n) {
-                const int i = 2 * n + kv, round = i / a.ring;
-                drain_wait(ring_full(i % a.ring, kv), (kQuant && (a.ring & 1) ? round >> 1 : round) & 1);
+            if (!ok) {  // let the copies already issued land before the CTA leaves
+                for (int n = max(tcnt - a.ring, 0); n < tcnt; ++n) {
+                    const int i = 2 * n + kv, round = i / a.ring;
+                    drain_wait(ring_full(i % a.ring, kv), (kQuant && (a.ring & 1) ? round >> 1 : round) & 1);
+                }
             }
-        }
-    } else if (warp < 4) {
-        if constexpr (Shape<QT, TYPE>::kSplitRegs)
-            reg_dec<Shape<QT, TYPE>::kControlRegs>();
-        if (warp == 1) {
+        } else if (warp == 1) {
             // ------------------------------------------------------------ MMA issuer
             // The warp walks and waits together and one elected lane issues: operands are then
             // warp-uniform for the compiler, which costs far less per MMA than a lone lane's.
