@@ -53,6 +53,7 @@
 #include <cstdint>
 #include <numeric>
 
+#include "attention_work.cuh"
 #include "f32x2.cuh"
 #include "internal.h"
 #include "paged.cuh"
@@ -63,7 +64,6 @@ namespace df2 {
 namespace {
 
 constexpr int BM = 128;  // rows of a tile
-constexpr int BN = 128;  // keys of a tile
 constexpr int HALF_BYTES = 128 * 128;  // 128 rows of 64 16-bit elements
 constexpr int SMEM_LIMIT = 227 * 1024;
 constexpr int MAX_RING = 12;
@@ -84,12 +84,11 @@ struct Args {
     float *lse;
     float scale_log2;
     uint32_t q_and, q_xor;  // scale 0 clears q, a negative one flips its sign
-    int causal, window, group;
+    WorkShape work;
+    int group;             // query heads of a cache head
     int q_wide, out_wide;  // rows begin on 32-byte borders
-    int tpm;   // tokens of a row tile
-    int span;  // tokens of an item
+    int tpm;               // tokens of a row tile
     uint32_t page_magic, page_shift;  // token / page_size = umulhi(token, magic) >> shift
-    int item_cost;  // key tiles that an item costs besides its own
     int box;   // rows of a TMA box: gcd(page_size, 128)
     int ring;  // stages of the TMA ring
     SplitRecord *records;
@@ -98,17 +97,14 @@ struct Args {
     uint32_t *status;
 };
 
-struct Sequence {
-    int start, n, len;
-};
-
 // token / page_size for 0 <= token < 2^31.
 __device__ __forceinline__ int page_of_token(const Args &a, int token)
 {
     return static_cast<int>(__umulhi(static_cast<uint32_t>(token), a.page_magic) >> a.page_shift);
 }
 
-constexpr int NEAR = 32;  // sequences whose numbers a CTA keeps in shared memory
+constexpr int NEAR = 32;              // sequences whose numbers a CTA keeps in shared memory
+constexpr uint32_t MANY = 0xFFFFFFFFu;  // units of a sequence that are counted anew where they are wanted
 
 __device__ __forceinline__ Sequence load_sequence(const Args &a, int b)
 {
@@ -118,147 +114,6 @@ __device__ __forceinline__ Sequence load_sequence(const Args &a, int b)
     s.len = min(max(__ldg(a.tokens.kv_len + b), 0), a.tokens.max_pages * a.cache.page_size);
     return s;
 }
-
-__device__ __forceinline__ Sequence sequence_at(const Args &a, const Sequence *near, int b)
-{
-    return b < NEAR ? near[b] : load_sequence(a, b);
-}
-
-struct Item {
-    int tok0, ntok;    // first token in its sequence, tokens
-    int p0;            // position of the first
-    int lo, hi;        // positions some row sees
-    int tile0, tiles;  // key tiles (one, empty, if nothing is seen)
-
-    __device__ __forceinline__ int units(const Args &a) const { return tiles + a.item_cost; }
-};
-
-__device__ __forceinline__ Item item_at(const Args &a, const Sequence &s, int qt)
-{
-    Item it;
-    it.tok0 = qt * a.span;
-    it.ntok = min(s.n - it.tok0, a.span);
-    it.p0 = s.len - s.n + it.tok0;
-    it.hi = a.causal ? min(s.len, it.p0 + it.ntok) : s.len;
-    it.lo = a.window > 0 ? max(0, it.p0 - a.window + 1) : 0;
-    if (it.hi <= it.lo) {
-        it.lo = it.hi = it.tile0 = 0;
-        it.tiles = 1;
-    } else {
-        it.tile0 = it.lo / BN;
-        it.tiles = (it.hi - 1) / BN - it.tile0 + 1;
-    }
-    return it;
-}
-
-__device__ __forceinline__ int items_of(const Args &a, const Sequence &s) { return (s.n + a.span - 1) / a.span; }
-
-// A run of key tiles of one item.
-struct Segment {
-    Item item;
-    int b, kvh, start;   // start: the sequence's first packed token
-    int tile, tiles;
-    int first, last;     // has the item's first / last tile
-    int slot;            // where a piece of an item goes
-    int end_cta;         // of an item that begins here and ends elsewhere: the CTA with its last tile
-};
-
-__device__ __forceinline__ long long quotient(long long a, int b)
-{
-    return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-
-// `units` cut into `grid` shares, share c beginning at floor(c units / grid).
-struct Shares {
-    long long units, each;
-    int grid, more;
-
-    __device__ __forceinline__ Shares(long long n, int g) : units(n), each(quotient(n, g)), grid(g)
-    {
-        more = static_cast<int>(n - each * g);
-    }
-    __device__ __forceinline__ long long begin(int c) const { return c * each + static_cast<unsigned>(c * more) / static_cast<unsigned>(grid); }
-    __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * grid - 1) / units); }
-};
-
-// The segments of a CTA's share [u, u_end) of the units, cache head by cache head, item by item.  An
-// item has a unit for each key tile and, before them, some for its queries, its first score and its
-// results: CTAs with short items would else finish last.
-// One warp walks and hands the segments to the others through shared memory: walking code in every
-// role made the loops too long for the instruction cache (warps waited for instructions half the time).
-struct Walk {
-    long long u, u_end;
-    int pieces = 0;
-    int b, kvh, qt, off, nq;
-    Sequence s;
-    const Sequence *near;
-
-    __device__ __forceinline__ void begin(const Args &a, const Sequence *near_, const int *prefix, const Shares &shares, int c)
-    {
-        near = near_;
-        u = shares.begin(c);
-        u_end = shares.begin(c + 1);
-        int lo = 0, hi = a.tokens.B;  // the largest b with prefix[b] * heads <= u
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (static_cast<long long>(prefix[mid]) * a.cache.heads <= u)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        b = lo;
-        s = sequence_at(a, near, b);
-        nq = items_of(a, s);
-        const unsigned per_head = max(prefix[b + 1] - prefix[b], 1);
-        const unsigned r = static_cast<unsigned>(u - static_cast<long long>(prefix[b]) * a.cache.heads);
-        kvh = static_cast<int>(r / per_head);
-        off = static_cast<int>(r - kvh * per_head);
-        for (qt = 0; qt + 1 < nq; ++qt) {
-            const int t = item_at(a, s, qt).units(a);
-            if (off < t)
-                break;
-            off -= t;
-        }
-    }
-
-    __device__ __forceinline__ void next(const Args &a, int cta, const Shares &shares, Segment &g)
-    {
-        g.tiles = 0;
-        while (g.tiles == 0 && u < u_end) {
-            while (kvh == a.cache.heads) {  // the next sequence that has tokens
-                ++b;
-                s = sequence_at(a, near, b);
-                nq = items_of(a, s);
-                kvh = nq > 0 ? 0 : a.cache.heads;
-            }
-            g.item = item_at(a, s, qt);
-            g.b = b;
-            g.kvh = kvh;
-            g.start = s.start;
-            const int n = static_cast<int>(min(static_cast<long long>(g.item.units(a) - off), u_end - u));
-            const int from = max(off - a.item_cost, 0), to = off + n - a.item_cost;
-            u += n;
-            off += n;
-            if (to > from) {
-                g.tile = g.item.tile0 + from;
-                g.tiles = to - from;
-                g.first = from == 0;
-                g.last = to == g.item.tiles;
-                g.slot = 2 * cta + pieces++;
-                if (g.first && !g.last)
-                    g.end_cta = shares.owner(u - off + g.item.units(a) - 1);
-            }
-            if (off == g.item.units(a)) {
-                off = 0;
-                if (++qt == nq) {
-                    qt = 0;
-                    ++kvh;
-                }
-            }
-        }
-        pieces = min(pieces, 1);  // only a CTA's first and last segments can be pieces
-    }
-};
 
 // Where one kind of operand is in a ring that both share: operand 2 j is tile j's K, 2 j + 1 its V,
 // operand i is in slot i mod size, for the (i / size)-th time.
@@ -345,9 +200,9 @@ struct Shape {
 };
 
 // Shared memory: Q tiles (two row tiles; one tile's queries are in TMEM) | TMA ring | widened ring
-// (8-bit) | scales, and as they lie (8-bit) | place to add copies up, their (m, l) | barriers | segments | sequences | prefix sums.
+// (8-bit) | scales, and as they lie (8-bit) | place to add copies up, their (m, l) | barriers | segments | sequences | their units.
 struct Layout {
-    int q, ring, ring_stage, wide, scales, raw, fold, bars, segs, near, prefix, bytes;
+    int q, ring, ring_stage, wide, scales, raw, fold, bars, segs, near, counts, bytes;
 };
 
 constexpr int BAR_COUNT = 4 * MAX_RING + 3 * MAX_WIDE + 2 + 2 + 2 + 2 + MAX_SCALES + 1 + 1 + 2 + 2 * SEGMENTS;  // tmem slot and abort flag follow
@@ -367,8 +222,8 @@ __host__ __device__ constexpr Layout layout_of(int ring, int dim, int B)
     l.bars = l.fold + (FOLD > 1 ? BM * 16 * 4 + BM * 8 : 0);
     l.segs = l.bars + BAR_COUNT * 8 + 8;
     l.near = l.segs + SEGMENTS * static_cast<int>(sizeof(Segment));
-    l.prefix = l.near + NEAR * static_cast<int>(sizeof(Sequence));
-    l.bytes = l.prefix + (B + 1) * 4;
+    l.counts = l.near + NEAR * static_cast<int>(sizeof(Sequence));
+    l.bytes = l.counts + B * 4;
     return l;
 }
 
@@ -494,7 +349,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     auto op_empty = [&](int s, int kv) { return kQuant ? wide_empty(s, kWide & 1 ? 1 - kv : kv) : ring_empty(s, a.ring & 1 ? 1 - kv : kv); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.bars + BAR_COUNT * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *prefix = reinterpret_cast<int *>(smem + lay.prefix);
+    uint32_t *counts = reinterpret_cast<uint32_t *>(smem + lay.counts);
     Sequence *near = reinterpret_cast<Sequence *>(smem + lay.near);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -543,39 +398,34 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
 
-    // Key tiles of each sequence (for one cache head), then, in warp 0, their running sum.  Up to 32
-    // sequences warp 0 does it alone and the others need not wait.
+    // Units of each sequence (for one cache head), as many as 32 bits hold.  Up to 32 sequences warp 0
+    // does it alone and the others need not wait.
     const int B = a.tokens.B;
-    auto tiles_of = [&](const Sequence &s, int first, int step) {
-        const int nq = items_of(a, s);
-        int t = 0;
-        for (int qt = first; qt < nq; qt += step)
-            t += item_at(a, s, qt).units(a);
-        return t;
-    };
+    auto sequence = [&](int b) { return b < NEAR ? near[b] : load_sequence(a, b); };
+    auto count = [&](int b, long long n) { counts[b] = static_cast<uint32_t>(min(n, static_cast<long long>(MANY))); };
     if (B > NEAR) {
         for (int b = threadIdx.x; b < B; b += kThreads) {
             const Sequence s = load_sequence(a, b);
             if (b < NEAR)
                 near[b] = s;
-            prefix[b + 1] = tiles_of(s, 0, 1);
+            count(b, units_of(a.work, s, 0, 1));
         }
         __syncthreads();
     } else if (warp == 0) {
         Sequence s{0, 0, 0};
         if (lane < B)
             near[lane] = s = load_sequence(a, lane);
-        if (__all_sync(0xffffffffu, items_of(a, s) <= 4)) {
+        if (__all_sync(0xffffffffu, items_of(a.work, s) <= 4)) {
             if (lane < B)
-                prefix[lane + 1] = tiles_of(s, 0, 1);
+                count(lane, units_of(a.work, s, 0, 1));
         } else {
             __syncwarp();
             for (int b = 0; b < B; ++b) {
-                int t = tiles_of(near[b], lane, 32);
+                long long t = units_of(a.work, near[b], lane, 32);
                 for (int o = 16; o > 0; o >>= 1)
                     t += __shfl_xor_sync(0xffffffffu, t, o);
                 if (lane == 0)
-                    prefix[b + 1] = t;
+                    count(b, t);
             }
         }
         __syncwarp();
@@ -601,32 +451,57 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             // issue their own boxes are taken one by one anyhow, at several times the cost.
             const int kv = warp == 0 ? 0 : 1;
             const CUtensorMap *map = kv ? &map_v : &map_k;
-            long long units = 0;
+            Shares shares(1, 1);
+            Walk walk;
+            walk.u = walk.u_end = 0;
             if (kv == 0) {
-                int sum = 0;
-                if (lane == 0)
-                    prefix[0] = 0;
-                for (int b0 = 0; b0 < B; b0 += 32) {
-                    int t = b0 + lane < B ? prefix[b0 + lane + 1] : 0;
+                auto units_in = [&](int b) -> long long {
+                    if (b >= B)
+                        return 0;
+                    const uint32_t n = counts[b];
+                    return n < MANY ? n : units_of(a.work, sequence(b), 0, 1);
+                };
+                auto running = [&](long long t) {  // this lane's and those of the lanes before it
                     for (int o = 1; o < 32; o <<= 1) {
-                        const int x = __shfl_up_sync(0xffffffffu, t, o);
+                        const long long x = __shfl_up_sync(0xffffffffu, t, o);
                         t += lane >= o ? x : 0;
                     }
-                    t += sum;
-                    if (b0 + lane < B)
-                        prefix[b0 + lane + 1] = t;
-                    sum = __shfl_sync(0xffffffffu, t, 31);
+                    return t;
+                };
+                // Sequences 32 at a time; a lane keeps what is ahead of runs `lane` and `lane + 32`.
+                long long sum = 0, mine = 0, upto = 0, ahead_lo = 0, ahead_hi = 0;
+                const int runs = (B + 31) / 32;
+                for (int i = 0; i < runs; ++i) {
+                    mine = units_in(32 * i + lane);
+                    upto = running(mine);
+                    if (lane == (i & 31)) {
+                        if (i < 32)
+                            ahead_lo = sum;
+                        else
+                            ahead_hi = sum;
+                    }
+                    sum += __shfl_sync(0xffffffffu, upto, 31);
                 }
-                __syncwarp();
-                units = static_cast<long long>(sum) * a.cache.heads;
+                const long long units = sum * a.work.heads;
+                const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(units, 1ll)));
+                shares = Shares(units, grid);
+                if (cta < grid && units > 0) {
+                    // the last run, and in it the last sequence, that begins at or before the share
+                    const long long u = shares.begin(cta);
+                    int run = 0;
+                    if (runs > 1) {
+                        run = __popc(__ballot_sync(0xffffffffu, lane < runs && ahead_lo * a.work.heads <= u)) +
+                              __popc(__ballot_sync(0xffffffffu, lane + 32 < runs && ahead_hi * a.work.heads <= u)) - 1;
+                        mine = units_in(32 * run + lane);
+                        upto = running(mine);
+                    }
+                    const long long ahead = __shfl_sync(0xffffffffu, run < 32 ? ahead_lo : ahead_hi, run & 31) + upto - mine;
+                    const uint32_t before = __ballot_sync(0xffffffffu, 32 * run + lane < B && ahead * a.work.heads <= u);
+                    const int at = 31 - __clz(before);
+                    walk.begin(a.work, sequence, u, shares.begin(cta + 1), 32 * run + at,
+                               __shfl_sync(0xffffffffu, ahead, at), __shfl_sync(0xffffffffu, mine, at));
+                }
             }
-            const int grid = static_cast<int>(min(static_cast<long long>(gridDim.x), max(units, 1ll)));
-            const Shares shares(units, grid);
-            Walk walk;
-            if (kv == 0 && cta < grid && units > 0)
-                walk.begin(a, near, prefix, shares, cta);
-            else
-                walk.u = walk.u_end = 0;
             const int boxes = BN / a.box, per_batch = 32 / boxes;  // boxes of a tile, tiles of a batch of 32
             const int ps = a.cache.page_size, dim = a.cache.dim;
             const uint32_t box_bytes = kQuant ? a.box * dim : a.box * 128 * kHalves;
@@ -641,7 +516,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     if (!ok)
                         break;
                     Segment next;
-                    walk.next(a, cta, shares, next);
+                    walk.next(a.work, sequence, cta, shares, next);
                     if (lane == 0) {
                         segs[n % SEGMENTS] = next;
                         mbar_arrive(seg_full(n % SEGMENTS));
@@ -1087,8 +962,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             int hi = 0x7FFFFFFF, lo = 0;  // rows of no token: whatever comes out goes nowhere
             if (live) {
                 const int pos = g.item.p0 + s * a.tpm + rt;
-                hi = a.causal ? min(g.item.hi, pos + 1) : g.item.hi;
-                lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+                hi = a.work.causal ? min(g.item.hi, pos + 1) : g.item.hi;
+                lo = a.work.window > 0 && pos >= a.work.window ? pos - a.work.window + 1 : 0;
             }
             float m = -INFINITY, l = 0.f;
             const float sl2 = kQuant ? 1.f : a.scale_log2;
@@ -1702,22 +1577,23 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.q_and = opt.scale == 0.f ? 0u : 0xFFFFFFFFu;
     a.q_xor = opt.scale < 0.f ? 0x80008000u : 0u;
-    a.causal = opt.causal;
+    a.work.causal = opt.causal;
     auto wide = [](const HeadRows &r) {
         return reinterpret_cast<uintptr_t>(r.data) % 32 == 0 && r.token_stride % 16 == 0 && r.head_stride % 16 == 0;
     };
     a.q_wide = wide(q);
     a.out_wide = wide(out);
-    a.window = opt.window >= tokens.max_pages * cache.page_size ? 0 : opt.window;
+    a.work.window = opt.window >= tokens.max_pages * cache.page_size ? 0 : opt.window;
     a.group = q.heads / cache.heads;
     const int tiles = row_tiles(tokens, a.group);
     const int fold = row_copies(cache, tokens, a.group);
     a.tpm = BM / fold / a.group;
-    a.span = tiles * a.tpm;
+    a.work.span = tiles * a.tpm;
+    a.work.heads = cache.heads;
     // Measured on GB300: 2048 tokens over their own 2048 keys (two row tiles) 100.7, 84.4, 76.5, 73.2,
     // 70.5 and 71.4 us at 0, 1, 2, 3, 4 and 6; 7 blocks of 16 over 1000 keys (one) 20.3, 17.4 and
     // 19.4 us at 0, 1 and 3.
-    a.item_cost = tiles == 2 ? 4 : 1;
+    a.work.item_cost = tiles == 2 ? 4 : 1;
     a.box = std::gcd(cache.page_size, BN);
     // ceil(2^(31 + b) / page_size) with b = ceil(log2(page_size)) gives the exact quotient below 2^31
     int bits = 3;
