@@ -559,10 +559,10 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     __syncwarp();
                     uint32_t dst = sbase + lay.ring + rs.slot * lay.ring_stage;
                     int in_page = tok - page_of_token(a, tok) * ps;
-    #pragma unroll 1
+#pragma unroll 1
                     for (int i = 0; i < boxes; i += 4) {
                         int page[4], x[4];
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             page[k] = __shfl_sync(0xffffffffu, batch, (at + i + k) & 31);
                             page[k] = i + k < boxes ? page[k] : -1;
@@ -571,14 +571,14 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             in_page = in_page == ps ? 0 : in_page;
                         }
                         if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 if (page[k] >= 0) {
                                     const uint32_t to = dst + k * a.box * (kQuant ? dim : 128);
                                     if constexpr (kQuant) {
                                         tma_load_4d(to, map, full, 0, x[k], kvh, page[k]);
                                     } else {
-    #pragma unroll
+#pragma unroll
                                         for (int h = 0; h < kHalves; ++h)
                                             tma_load_4d(to + h * HALF_BYTES, map, full, h * 64, x[k], kvh, page[k]);
                                     }
