@@ -272,14 +272,18 @@ __device__ __forceinline__ void store2(uint32_t *v, uint64_t x)
 // A converged warp's wait for the phase of parity `parity`; false when another role gave up, or
 // after kWaitCycles, when it gives up itself.  (As short as it can be: it is inlined everywhere.)
 constexpr long long kWaitCycles = 2000000000;  // about a second
+// For warps that have no part in an item while the others work through all of its tiles: up to 2^23 of
+// them, a microsecond and more each.  Should one of the others give up, these see its flag.
+constexpr long long kIdleCycles = 64 * kWaitCycles;
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                          long long limit = kWaitCycles)
 {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
         return true;
     const long long t0 = clock64();
     while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-        if (__any_sync(0xffffffffu, *abort_flag != 0 || clock64() - t0 > kWaitCycles)) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || clock64() - t0 > limit)) {
             *abort_flag = 1;
             return false;
         }
@@ -433,7 +437,9 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
     const int cta = blockIdx.x;
     Segment *segs = reinterpret_cast<Segment *>(smem + lay.segs);
     // the CTA's n-th segment (tiles == 0: there is none), and done with it
-    auto seg_wait = [&](int n) { return warp_wait(seg_full(n % SEGMENTS), (n / SEGMENTS) & 1, abort_flag); };
+    auto seg_wait = [&](int n, long long limit = kWaitCycles) {
+        return warp_wait(seg_full(n % SEGMENTS), (n / SEGMENTS) & 1, abort_flag, limit);
+    };
     auto seg_done = [&](int n) {
         __syncwarp();
         if (lane == 0)
@@ -1173,7 +1179,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 break;
             // the next item's queries go in while the last product of this one runs
             const Segment &next = segs[(n + 1) & (SEGMENTS - 1)];
-            ok = seg_wait(n + 1);
+            ok = seg_wait(n + 1, QT == 2 && !act ? kIdleCycles : kWaitCycles);
             if (!ok)
                 break;
             more = next.tiles != 0;
