@@ -3,6 +3,7 @@
 // (except dflash2_check_device_status and dflash2_select_host).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -46,9 +47,17 @@ cudaError_t ensure_dynamic_smem(const void *kernel, int bytes)
     for (int i = 0; i < used; ++i)
         if (seen[i].kernel == kernel && seen[i].dev == dev && seen[i].bytes >= bytes)
             return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess)
-        return e;
+    {
+        // The attribute is the process's, and other threads launch with sizes of their own: it is only
+        // ever raised, so what a thread has seen suffice goes on sufficing.
+        static std::mutex mu;
+        std::lock_guard<std::mutex> lock(mu);
+        cudaFuncAttributes attr{};
+        if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      std::max(bytes, attr.maxDynamicSharedSizeBytes))) != cudaSuccess)
+            return e;
+    }
     seen[next] = Entry{kernel, dev, bytes};
     next = (next + 1) % kEntries;
     used = used < kEntries ? used + 1 : kEntries;

@@ -295,8 +295,8 @@ cudaError_t launch_rows(ConvArgs a, cudaStream_t stream)
     a.tiles_per_block = (a.T + kRows - 1) / kRows;
     a.n_tiles = a.B * a.tiles_per_block;
     const size_t smem = buffer_bytes<kRows>(a.C, a.G);
-    const cudaError_t e = cudaFuncSetAttribute(dynamic_conv_kernel<kRows>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(dynamic_conv_kernel<kRows>),
+                                              static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};

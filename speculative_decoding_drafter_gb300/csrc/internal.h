@@ -26,8 +26,8 @@ inline int kp_for(int k) { return k <= 4 ? 4 : k <= 8 ? 8 : k <= 16 ? 16 : 32; }
 // Streaming multiprocessors of the current device (cached per device).
 int device_sm_count();
 
-// Opts `kernel` in to at least `bytes` of dynamic shared memory on the current device; the
-// attribute is set once per kernel, device and size (remembered per host thread).
+// Opts `kernel` in to at least `bytes` of dynamic shared memory on the current device.  The
+// attribute is the process's and is only ever raised; a host thread remembers what it has asked for.
 cudaError_t ensure_dynamic_smem(const void *kernel, int bytes);
 
 // LM head (and gate) in one tensor-core launch: C = hidden[R, K] . [W_vocab; W_store]^T

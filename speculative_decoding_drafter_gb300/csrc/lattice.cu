@@ -81,8 +81,8 @@ cudaError_t launch_lattice_kp(int B, int T, int k, int V, int D, const int32_t *
 {
     // dynamic part only; the kernel's static arrays come on top, so the opt-in is always set
     const size_t smem = lattice_smem_bytes(k, D);
-    const cudaError_t e = cudaFuncSetAttribute(lattice_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(lattice_kernel<KP>),
+                                              static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
     lattice_kernel<KP><<<static_cast<unsigned>(B * T), kLatticeThreads, smem, stream>>>(T, k, V, D, ids, vals, gate,

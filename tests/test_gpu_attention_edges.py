@@ -1,10 +1,11 @@
 """Attention over the paged cache where numbers, sizes or callers are at an edge, on the GPU against float64."""
 import math
+import threading
 
 import pytest
 import torch
 
-from attention_rules import BF16
+from attention_rules import BF16, Batch
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,52 @@ def at():
 
 def randn(seed, *shape):
     return torch.randn(*shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed))
+
+
+def one_sequence(at, k, v, dtype, page_size=64, copies=1, new=1):
+    """A cache that holds k and v [n, heads, dim], as `copies` sequences over the same pages; its batch of `new` tokens
+    each, and the rows as held, in float64."""
+    n, heads, dim = k.shape
+    b = Batch([n], [n], page_size, spare=0)
+    cache = at.PagedCache.allocate(b.pages, page_size, heads, dim, dtype)
+    at.dflash2_cache_append(cache, b.on_gpu(at), k.to(BF16), v.to(BF16))
+    p = torch.arange(n, device="cuda")
+    pages, slots = b.table.cuda()[0][p // page_size].long(), p % page_size
+    rows = []
+    for name in ("k", "v"):
+        if dtype == BF16:
+            rows.append(getattr(cache, name)[pages, :, slots].double())
+        else:
+            r = getattr(cache, name).view(torch.uint8)[pages, :, slots].view(dtype).double()
+            rows.append(r * getattr(cache, name + "_scale")[pages, :, slots].double()[..., None])
+    batch = at.TokenBatch(torch.arange(copies + 1, dtype=torch.int32, device="cuda") * new,
+                          torch.full((copies,), n, dtype=torch.int32, device="cuda"),
+                          b.table.expand(copies, -1).contiguous().cuda(), tokens=copies * new, max_new=new)
+    return cache, batch, rows[0], rows[1]
+
+
+# ------------------------------------------------------------------------------------------ callers
+
+
+def test_calls_of_several_sizes_from_two_threads(at):
+    """What a call needs of the device does not depend on what another thread called before."""
+    k, v = randn(1, 100, 2, 128), randn(2, 100, 2, 128)
+    failed = []
+
+    def call(copies):
+        try:
+            cache, batch, _, _ = one_sequence(at, k, v, BF16, copies=copies)
+            at.dflash2_paged_attention(randn(3, copies, 4, 128).to(BF16), cache, batch)
+        except Exception as e:  # noqa: BLE001
+            failed.append((copies, repr(e)))
+
+    call(32)
+    other = threading.Thread(target=call, args=(1,))
+    other.start()
+    other.join()
+    call(32)
+    torch.cuda.synchronize()
+    assert not failed
 
 
 # ------------------------------------------------------------------------------------------ waits
