@@ -92,7 +92,7 @@ struct Args {
     int box;   // rows of a TMA box: gcd(page_size, 128)
     int ring;  // stages of the TMA ring
     SplitRecord *records;
-    float2 *part_ml;  // [2 * grid][rows]: (maximum in powers of two, sum)
+    float2 *part_ml;  // [2 * grid][rows]: (maximum, logarithm of the sum), in powers of two
     float *part_o;    // [2 * grid][rows][dim]
     uint32_t *status;
 };
@@ -154,6 +154,13 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// log2(2^a + 2^b)
+__device__ __forceinline__ float log_sum(float a, float b)
+{
+    const float top = fmaxf(a, b);
+    return top + __log2f(ex2(a - top) + ex2(b - top));
 }
 
 __device__ __forceinline__ uint32_t f16_pack(float a, float b)
@@ -971,206 +978,215 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 hi = a.work.causal ? min(g.item.hi, pos + 1) : g.item.hi;
                 lo = a.work.window > 0 && pos >= a.work.window ? pos - a.work.window + 1 : 0;
             }
-            float m = -INFINITY, l = 0.f;
+            // With an 8-bit cache a row of zeros, or of values next to the least, adds up to 2^116 to l, which
+            // holds a few thousand of them.  What would not fit goes to log_more, a logarithm that no move touches.
+            float m = -INFINITY, l = 0.f, log_more = -INFINITY;
             const float sl2 = kQuant ? 1.f : a.scale_log2;
             if (act) {
-                for (int j = 0; j < g.tiles; ++j) {
-                    const int t0 = (g.tile + j) * BN;
-                    const int sbuf = QT == 2 ? s : cnt & 1;
-                    const uint32_t s_phase = QT == 2 ? cnt & 1 : (cnt >> 1) & 1;
-                    ok = warp_wait(s_full(sbuf), s_phase, abort_flag);
-                    if (!ok)
-                        break;
-                    if constexpr (kQuant) {
-                        ok = warp_wait(scale_full(tcnt % kScales), (tcnt / kScales) & 1, abort_flag);
+                for (int j = 0, stop; ok && j < g.tiles;) {
+                    stop = kQuant ? min(g.tiles, j + 16) : g.tiles;  // a tile adds at most 2^123 to l
+                    for (; j < stop; ++j) {
+                        const int t0 = (g.tile + j) * BN;
+                        const int sbuf = QT == 2 ? s : cnt & 1;
+                        const uint32_t s_phase = QT == 2 ? cnt & 1 : (cnt >> 1) & 1;
+                        ok = warp_wait(s_full(sbuf), s_phase, abort_flag);
                         if (!ok)
                             break;
-                    }
-                    tc_fence_after();
-                    const uint32_t s_addr = lane_base + sbuf * BN;
-                    const uint32_t scales = sbase + lay.scales + ((tcnt % kScales) * 3 * BN + col0) * 4;
-                    if (warp_live) {
-                        // An 8-bit cache's scores of 128 keys do not fit the registers beside everything
-                        // else: scaled, they go back to TMEM until the maximum is known.
-                        constexpr bool kKeep = !kQuant || kCols <= 64;
-                        uint32_t v[kKeep ? kCols / 32 : 1][32];
-                        const int rlo = lo - t0 - col0, rhi = hi - t0 - col0;
-                        const bool edge = __any_sync(0xffffffffu, rlo > 0 || rhi < kCols);
-                        // keys c0 .. c0 + 31 that the row sees, a bit each; the others' scores go
-                        auto mask = [&](uint32_t(&x)[32], int c0) {
-                            const int below = min(max(rlo - c0, 0), 32), up_to = min(max(rhi - c0, 0), 32);
-                            const uint32_t seen = static_cast<uint32_t>((1ull << up_to) - 1) &
-                                                  ~static_cast<uint32_t>((1ull << below) - 1);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(seen & (1u << c)))
-                                    x[c] = 0xFF800000u;
-                        };
-                        // x_j of 32 keys from c0 (of this copy's), their S taken out of TMEM into x
-                        auto scores = [&](uint32_t(&x)[32], int c0) {
-                            tmem_ld_32x32b_x32(s_addr + col0 + c0, x);
-                            if constexpr (kQuant) {
-                                float4 ks[8], lv[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    ks[i] = lds4(scales + (c0 + 4 * i) * 4);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    lv[i] = lds4(scales + (BN + c0 + 4 * i) * 4);
-                                tmem_wait_ld(x);
-                                const uint64_t qs2 = f2(qscale, qscale);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    store2(x + 4 * i, fma2(mul2(load2(x + 4 * i), f2(ks[i].x, ks[i].y)), qs2,
-                                                           f2(lv[i].x, lv[i].y)));
-                                    store2(x + 4 * i + 2, fma2(mul2(load2(x + 4 * i + 2), f2(ks[i].z, ks[i].w)), qs2,
-                                                               f2(lv[i].z, lv[i].w)));
-                                }
-                            } else {
-                                tmem_wait_ld(x);
-                            }
-                            if (edge)
-                                mask(x, c0);
-                        };
-                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        auto raise = [&](const uint32_t(&x)[32]) {
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    top[i] = fmaxf(top[i], fmaxf(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])));
-                        };
                         if constexpr (kQuant) {
-#pragma unroll(kKeep ? 4 : 1)
-                            for (int i = 0; i < kCols / 32; ++i) {
-                                scores(v[kKeep ? i : 0], 32 * i);
-                                raise(v[kKeep ? i : 0]);
-                                if constexpr (!kKeep)
-                                    tmem_st_32x32b_x32(s_addr + col0 + 32 * i, v[0]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kCols / 32; ++i)
-                                tmem_ld_32x32b_x32(s_addr + col0 + 32 * i, v[i]);
-#pragma unroll
-                            for (int i = 0; i < kCols / 32; ++i)
-                                tmem_wait_ld(v[i]);
-                            if (edge) {
-#pragma unroll
-                                for (int i = 0; i < kCols / 32; ++i)
-                                    mask(v[i], 32 * i);
-                            }
-#pragma unroll
-                            for (int i = 0; i < kCols / 32; ++i)
-                                raise(v[i]);
-                        }
-                        if constexpr (!kKeep)
-                            tmem_wait_st();
-                        const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                        const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
-                        const bool move = live && rise > LAZY;
-                        if (j > 0 && __any_sync(0xffffffffu, move)) {
-                            // the products so far must be in before they are scaled
-                            ok = products_in();
+                            ok = warp_wait(scale_full(tcnt % kScales), (tcnt / kScales) & 1, abort_flag);
                             if (!ok)
                                 break;
-                            tc_fence_after();
-                            const float keep = move ? ex2(-rise) : 1.f;
-                            l = kQuant && move ? l * ex2(-0.5f * rise) * ex2(-0.5f * rise) : l * keep;
-#pragma unroll 1
-                            for (int c = 0; c < DP; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld_32x32b_x16(lane_base + 256 + s * 128 + c, o);
-                                tmem_wait_ld(o);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
-                                tmem_st_32x32b_x16(lane_base + 256 + s * 128 + c, o);
-                            }
                         }
-                        if (move)
-                            m = tile_top;
-                        const float base = m == -INFINITY ? 0.f : -m * sl2;
-                        const uint64_t base2 = f2(base, base), sl22 = f2(sl2, sl2);
-                        uint64_t sum2[2] = {0, 0};
-                        if constexpr (FOLD > 1) {  // the other copies' keys
-                            uint32_t z[16];
+                        tc_fence_after();
+                        const uint32_t s_addr = lane_base + sbuf * BN;
+                        const uint32_t scales = sbase + lay.scales + ((tcnt % kScales) * 3 * BN + col0) * 4;
+                        if (warp_live) {
+                            // An 8-bit cache's scores of 128 keys do not fit the registers beside everything
+                            // else: scaled, they go back to TMEM until the maximum is known.
+                            constexpr bool kKeep = !kQuant || kCols <= 64;
+                            uint32_t v[kKeep ? kCols / 32 : 1][32];
+                            const int rlo = lo - t0 - col0, rhi = hi - t0 - col0;
+                            const bool edge = __any_sync(0xffffffffu, rlo > 0 || rhi < kCols);
+                            // keys c0 .. c0 + 31 that the row sees, a bit each; the others' scores go
+                            auto mask = [&](uint32_t(&x)[32], int c0) {
+                                const int below = min(max(rlo - c0, 0), 32), up_to = min(max(rhi - c0, 0), 32);
+                                const uint32_t seen = static_cast<uint32_t>((1ull << up_to) - 1) &
+                                                      ~static_cast<uint32_t>((1ull << below) - 1);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                z[k] = 0;
-#pragma unroll
-                            for (int c = 0; c < BN / 2; c += 16)
-                                if (2 * c < col0 || 2 * c >= col0 + kCols)
-                                    tmem_st_32x32b_x16(s_addr + c, z);
-                        }
-#pragma unroll(kKeep ? 4 : 1)
-                        for (int c0 = 0; c0 < kCols; c0 += 32) {
-                            uint32_t p[16];
-                            float4 rv[8];
-                            if constexpr (kQuant) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    rv[i] = lds4(scales + (2 * BN + c0 + 4 * i) * 4);
-                            }
-                            if constexpr (!kKeep) {  // P goes where x has been read already
-                                tmem_ld_32x32b_x32(s_addr + col0 + c0, v[0]);
-                                tmem_wait_ld(v[0]);
-                            }
-                            const uint32_t(&vc)[32] = v[kKeep ? c0 / 32 : 0];
-#pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                uint64_t x0 = load2(vc + c), x1 = load2(vc + c + 2);
+                                for (int c = 0; c < 32; ++c)
+                                    if (!(seen & (1u << c)))
+                                        x[c] = 0xFF800000u;
+                            };
+                            // x_j of 32 keys from c0 (of this copy's), their S taken out of TMEM into x
+                            auto scores = [&](uint32_t(&x)[32], int c0) {
+                                tmem_ld_32x32b_x32(s_addr + col0 + c0, x);
                                 if constexpr (kQuant) {
-                                    x0 = add2(x0, base2), x1 = add2(x1, base2);
-                                } else {
-                                    x0 = fma2(x0, sl22, base2), x1 = fma2(x1, sl22, base2);
-                                }
-                                const float2 y0 = f2_split(x0), y1 = f2_split(x1);
-                                const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
-                                if constexpr (kQuant) {
-                                    sum2[0] = fma2(f2(p0, p1), f2(rv[c / 4].x, rv[c / 4].y), sum2[0]);
-                                    sum2[1] = fma2(f2(p2, p3), f2(rv[c / 4].z, rv[c / 4].w), sum2[1]);
-                                    p[c / 2] = f16_pack(p0, p1), p[c / 2 + 1] = f16_pack(p2, p3);
-                                } else {
-                                    sum2[0] = add2(sum2[0], f2(p0, p1));
-                                    sum2[1] = add2(sum2[1], f2(p2, p3));
-                                    p[c / 2] = bf16_pack(p0, p1), p[c / 2 + 1] = bf16_pack(p2, p3);
-                                }
-                            }
-                            tmem_st_32x32b_x16(s_addr + (col0 + c0) / 2, p);
-                        }
-                        const float2 sums = f2_split(add2(sum2[0], sum2[1]));
-                        l += sums.x + sums.y;
-                        tmem_wait_st();
-                    }
-                    if constexpr (!kQuant) {
-                        // rows of V that no row of the item sees may hold anything: 0 * NaN must not happen
-                        if (s == 0 && (t0 < g.item.lo || t0 + BN > g.item.hi)) {
-                            ok = warp_wait(ring_full(vr.slot, 0), vr.phase, abort_flag);
-                            if (!ok)
-                                break;
-                            if (t0 + row < g.item.lo || t0 + row >= g.item.hi) {
-                                uint8_t *vrow = smem + lay.ring + vr.slot * lay.ring_stage + row * 128;
-#pragma unroll
-                                for (int h = 0; h < kHalves; ++h)
+                                    float4 ks[8], lv[8];
 #pragma unroll
                                     for (int i = 0; i < 8; ++i)
-                                        *reinterpret_cast<uint4 *>(vrow + h * HALF_BYTES + 16 * i) =
-                                            make_uint4(0, 0, 0, 0);
+                                        ks[i] = lds4(scales + (c0 + 4 * i) * 4);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        lv[i] = lds4(scales + (BN + c0 + 4 * i) * 4);
+                                    tmem_wait_ld(x);
+                                    const uint64_t qs2 = f2(qscale, qscale);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        store2(x + 4 * i, fma2(mul2(load2(x + 4 * i), f2(ks[i].x, ks[i].y)), qs2,
+                                                               f2(lv[i].x, lv[i].y)));
+                                        store2(x + 4 * i + 2, fma2(mul2(load2(x + 4 * i + 2), f2(ks[i].z, ks[i].w)), qs2,
+                                                                   f2(lv[i].z, lv[i].w)));
+                                    }
+                                } else {
+                                    tmem_wait_ld(x);
+                                }
+                                if (edge)
+                                    mask(x, c0);
+                            };
+                            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            auto raise = [&](const uint32_t(&x)[32]) {
+#pragma unroll
+                                for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        top[i] = fmaxf(top[i], fmaxf(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])));
+                            };
+                            if constexpr (kQuant) {
+#pragma unroll(kKeep ? 4 : 1)
+                                for (int i = 0; i < kCols / 32; ++i) {
+                                    scores(v[kKeep ? i : 0], 32 * i);
+                                    raise(v[kKeep ? i : 0]);
+                                    if constexpr (!kKeep)
+                                        tmem_st_32x32b_x32(s_addr + col0 + 32 * i, v[0]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < kCols / 32; ++i)
+                                    tmem_ld_32x32b_x32(s_addr + col0 + 32 * i, v[i]);
+#pragma unroll
+                                for (int i = 0; i < kCols / 32; ++i)
+                                    tmem_wait_ld(v[i]);
+                                if (edge) {
+#pragma unroll
+                                    for (int i = 0; i < kCols / 32; ++i)
+                                        mask(v[i], 32 * i);
+                                }
+#pragma unroll
+                                for (int i = 0; i < kCols / 32; ++i)
+                                    raise(v[i]);
                             }
-                            fence_proxy_async();
+                            if constexpr (!kKeep)
+                                tmem_wait_st();
+                            const float tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                            const float rise = tile_top > m ? (tile_top - m) * sl2 : 0.f;  // inf from -inf
+                            const bool move = live && rise > LAZY;
+                            if (j > 0 && __any_sync(0xffffffffu, move)) {
+                                // the products so far must be in before they are scaled
+                                ok = products_in();
+                                if (!ok)
+                                    break;
+                                tc_fence_after();
+                                const float keep = move ? ex2(-rise) : 1.f;
+                                l = kQuant && move ? l * ex2(-0.5f * rise) * ex2(-0.5f * rise) : l * keep;
+#pragma unroll 1
+                                for (int c = 0; c < DP; c += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld_32x32b_x16(lane_base + 256 + s * 128 + c, o);
+                                    tmem_wait_ld(o);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        o[k] = __float_as_uint(__uint_as_float(o[k]) * keep);
+                                    tmem_st_32x32b_x16(lane_base + 256 + s * 128 + c, o);
+                                }
+                            }
+                            if (move)
+                                m = tile_top;
+                            const float base = m == -INFINITY ? 0.f : -m * sl2;
+                            const uint64_t base2 = f2(base, base), sl22 = f2(sl2, sl2);
+                            uint64_t sum2[2] = {0, 0};
+                            if constexpr (FOLD > 1) {  // the other copies' keys
+                                uint32_t z[16];
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    z[k] = 0;
+#pragma unroll
+                                for (int c = 0; c < BN / 2; c += 16)
+                                    if (2 * c < col0 || 2 * c >= col0 + kCols)
+                                        tmem_st_32x32b_x16(s_addr + c, z);
+                            }
+#pragma unroll(kKeep ? 4 : 1)
+                            for (int c0 = 0; c0 < kCols; c0 += 32) {
+                                uint32_t p[16];
+                                float4 rv[8];
+                                if constexpr (kQuant) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        rv[i] = lds4(scales + (2 * BN + c0 + 4 * i) * 4);
+                                }
+                                if constexpr (!kKeep) {  // P goes where x has been read already
+                                    tmem_ld_32x32b_x32(s_addr + col0 + c0, v[0]);
+                                    tmem_wait_ld(v[0]);
+                                }
+                                const uint32_t(&vc)[32] = v[kKeep ? c0 / 32 : 0];
+#pragma unroll
+                                for (int c = 0; c < 32; c += 4) {
+                                    uint64_t x0 = load2(vc + c), x1 = load2(vc + c + 2);
+                                    if constexpr (kQuant) {
+                                        x0 = add2(x0, base2), x1 = add2(x1, base2);
+                                    } else {
+                                        x0 = fma2(x0, sl22, base2), x1 = fma2(x1, sl22, base2);
+                                    }
+                                    const float2 y0 = f2_split(x0), y1 = f2_split(x1);
+                                    const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+                                    if constexpr (kQuant) {
+                                        sum2[0] = fma2(f2(p0, p1), f2(rv[c / 4].x, rv[c / 4].y), sum2[0]);
+                                        sum2[1] = fma2(f2(p2, p3), f2(rv[c / 4].z, rv[c / 4].w), sum2[1]);
+                                        p[c / 2] = f16_pack(p0, p1), p[c / 2 + 1] = f16_pack(p2, p3);
+                                    } else {
+                                        sum2[0] = add2(sum2[0], f2(p0, p1));
+                                        sum2[1] = add2(sum2[1], f2(p2, p3));
+                                        p[c / 2] = bf16_pack(p0, p1), p[c / 2 + 1] = bf16_pack(p2, p3);
+                                    }
+                                }
+                                tmem_st_32x32b_x16(s_addr + (col0 + c0) / 2, p);
+                            }
+                            const float2 sums = f2_split(add2(sum2[0], sum2[1]));
+                            l += sums.x + sums.y;
+                            tmem_wait_st();
                         }
-                        vr.step(a.ring);
+                        if constexpr (!kQuant) {
+                            // rows of V that no row of the item sees may hold anything: 0 * NaN must not happen
+                            if (s == 0 && (t0 < g.item.lo || t0 + BN > g.item.hi)) {
+                                ok = warp_wait(ring_full(vr.slot, 0), vr.phase, abort_flag);
+                                if (!ok)
+                                    break;
+                                if (t0 + row < g.item.lo || t0 + row >= g.item.hi) {
+                                    uint8_t *vrow = smem + lay.ring + vr.slot * lay.ring_stage + row * 128;
+#pragma unroll
+                                    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i)
+                                            *reinterpret_cast<uint4 *>(vrow + h * HALF_BYTES + 16 * i) =
+                                                make_uint4(0, 0, 0, 0);
+                                }
+                                fence_proxy_async();
+                            }
+                            vr.step(a.ring);
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(p_full(sbuf));
+                            if (kQuant && s == 0)
+                                mbar_arrive(soft_done(tcnt & 1));
+                        }
+                        ++cnt;
+                        ++tcnt;
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(p_full(sbuf));
-                        if (kQuant && s == 0)
-                            mbar_arrive(soft_done(tcnt & 1));
+                    if (kQuant && l > 0x1p80f) {
+                        log_more = log_sum(log_more, m + __log2f(l));
+                        l = 0.f;
                     }
-                    ++cnt;
-                    ++tcnt;
                 }
             } else if (started) {
                 tcnt += g.tiles;
@@ -1201,31 +1217,46 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 break;
             tc_fence_after();
             float weight = 1.f;
+            float log_l = log2f(l);
+            if constexpr (kQuant) {
+                if (log_more > -INFINITY)
+                    log_l = log_sum(log_l, log_more - m);
+            }
             if constexpr (FOLD > 1) {
                 // the copies' common maximum; each copy's weight; the sum of their sums
                 float2 *ml = reinterpret_cast<float2 *>(smem + lay.fold + BM * 16 * 4);
-                ml[row] = make_float2(m * sl2, l);
+                ml[row] = make_float2(m, log_l);
                 ok = group_sync();
                 if (!ok)
                     break;
-                float top = -INFINITY;
-#pragma unroll
-                for (int f = 0; f < FOLD; ++f)
-                    top = fmaxf(top, ml[f * kRows + trow].x);
-                const float b = top == -INFINITY ? 0.f : top;
-                weight = exp2f(m * sl2 - b);
-                l = 0.f;
+                float top = -INFINITY, far = -INFINITY;
 #pragma unroll
                 for (int f = 0; f < FOLD; ++f) {
                     const float2 x = ml[f * kRows + trow];
-                    // in one power, as in the combine kernel
-                    l += x.y > 0.f ? exp2f(x.x - b + log2f(x.y)) : x.y == 0.f ? 0.f : x.y;
+                    top = fmaxf(top, x.x);
+                    far = fmaxf(far, x.x + x.y);
                 }
+                const float b = top == -INFINITY ? 0.f : top;
+                weight = exp2f(m - b);
+                far = far == -INFINITY ? 0.f : far - b;
+                float sum = 0.f;
+#pragma unroll
+                for (int f = 0; f < FOLD; ++f) {
+                    const float2 x = ml[f * kRows + trow];
+                    sum += exp2f(x.x - b + x.y - far);  // in one power, as in the combine kernel
+                }
+                log_l = far + log2f(sum);
                 m = top;
             } else {
                 m *= sl2;
             }
-            const float inv = whole ? (l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l) : 1.f;
+            float inv = 1.f;
+            if (whole) {
+                if constexpr (kQuant)
+                    inv = log_l == -INFINITY ? 0.f : exp2f(-log_l);
+                else
+                    inv = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;
+            }
             if (warp_live || FOLD > 1) {
                 constexpr int kChunk = FOLD > 1 ? 16 : 32;     // columns at a time
                 constexpr int kPer = kChunk / FOLD;            // ... of which this thread writes
@@ -1295,9 +1326,9 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             }
             if (live && col0 == 0) {
                 if (!whole)
-                    a.part_ml[part] = make_float2(m, l);
+                    a.part_ml[part] = make_float2(m, log_l);
                 else if (a.lse)
-                    a.lse[static_cast<long long>(tok) * a.q.heads + head] = (m + log2f(l)) * 0.69314718055994530942f;
+                    a.lse[static_cast<long long>(tok) * a.q.heads + head] = (m + log_l) * 0.69314718055994530942f;
             }
             if (s == 0 && row == 0 && g.first && !g.last) {
                 SplitRecord rec;
@@ -1425,13 +1456,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ar
 #pragma unroll
     for (int i = 0; i < kEarly; ++i)
         early[i] = piece(i);
-    float2 ml = lane < n ? a.part_ml[at(lane)] : make_float2(-INFINITY, 0.f);
-    float top = ml.x;
-    for (int i = lane + 32; i < n; i += 32)
-        top = fmaxf(top, a.part_ml[at(i)].x);
+    float2 ml = lane < n ? a.part_ml[at(lane)] : make_float2(-INFINITY, -INFINITY);
+    float top = ml.x, far = ml.x + ml.y;
+    for (int i = lane + 32; i < n; i += 32) {
+        const float2 x = a.part_ml[at(i)];
+        top = fmaxf(top, x.x);
+        far = fmaxf(far, x.x + x.y);
+    }
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float base = top == -INFINITY ? 0.f : top;
+    // with an 8-bit cache the maximum carries a value's scale and a sum may be far from it
+    if (a.cache.type != 0) {
+        for (int o = 16; o > 0; o >>= 1)
+            far = fmaxf(far, __shfl_xor_sync(0xffffffffu, far, o));
+        far = far == -INFINITY ? 0.f : far - base;
+    } else {
+        far = 0.f;
+    }
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float w, const float4 &o) {
@@ -1440,11 +1482,9 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ar
     };
     for (int i0 = 0; i0 < n; i0 += 32) {
         if (i0 > 0)
-            ml = i0 + lane < n ? a.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
+            ml = i0 + lane < n ? a.part_ml[at(i0 + lane)] : make_float2(-INFINITY, -INFINITY);
         const float wgt = exp2f(ml.x - base);
-        // in one power: with an 8-bit cache the maximum carries a value's scale, and the weight
-        // alone may fall below what float32 holds
-        l += ml.y > 0.f ? exp2f(ml.x - base + log2f(ml.y)) : ml.y == 0.f ? 0.f : ml.y;
+        l += exp2f(ml.x - base + ml.y - far);  // in one power: the weight alone may fall below what float32 holds
         int i = 0;
         if (i0 == 0) {
 #pragma unroll
@@ -1458,14 +1498,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Ar
     }
     for (int o = 16; o > 0; o >>= 1)
         l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+    const float inv = l > 0.f ? exp2f(-far) / l : l == 0.f ? 0.f : l;
     const long long token = rec.tok0 + t;
     const int head = rec.kvh * a.group + gi;
     if (4 * lane < dim)
         *reinterpret_cast<uint2 *>(a.out.data + token * a.out.token_stride + head * a.out.head_stride + 4 * lane) =
             make_uint2(bf16_pack(acc.x * inv, acc.y * inv), bf16_pack(acc.z * inv, acc.w * inv));
     if (a.lse && lane == 0)
-        a.lse[token * a.q.heads + head] = (top + log2f(l)) * 0.69314718055994530942f;
+        a.lse[token * a.q.heads + head] = (top + (far + log2f(l))) * 0.69314718055994530942f;
 }
 
 // Row tiles an item has: two when some sequence may have more rows than one holds.

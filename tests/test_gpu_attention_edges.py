@@ -5,9 +5,12 @@ import threading
 import pytest
 import torch
 
-from attention_rules import BF16, Batch
+from attention_rules import BF16, Batch, attend, attend_bound
 
 pytestmark = pytest.mark.gpu
+
+E4M3, INT8 = torch.float8_e4m3fn, torch.int8
+EIGHT_BITS = pytest.mark.parametrize("dtype", [E4M3, INT8])
 
 
 @pytest.fixture(scope="module")
@@ -43,6 +46,16 @@ def one_sequence(at, k, v, dtype, page_size=64, copies=1, new=1):
     return cache, batch, rows[0], rows[1]
 
 
+def lse_close(got, want):
+    """float32 scores of size up to 2^4 summed over dim terms, and a sum of positive terms."""
+    return ((got.double() - want).abs() <= 2.0 ** -14 * (1 + want.abs())).all()
+
+
+def unit_scale(dim):
+    """The scale at which a key of c's scores c powers of two with a query of ones."""
+    return 1.0 / (dim * math.log2(math.e))
+
+
 # ------------------------------------------------------------------------------------------ callers
 
 
@@ -65,6 +78,28 @@ def test_calls_of_several_sizes_from_two_threads(at):
     call(32)
     torch.cuda.synchronize()
     assert not failed
+
+
+# ------------------------------------------------------------------------------------------ numbers
+
+
+@EIGHT_BITS
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("size", [2.0 ** -90, 1.0, 2.0 ** 110])
+def test_sum_over_many_rows_of_zeros(at, dtype, new, size):
+    """Thousands of value rows of zeros before the first that is not, their scores just under what moves the running
+    maximum: the sum of the exponentials leaves float32's range if it is held in units of an unknown scale."""
+    dim, heads, copies = 64, 8, 19  # an item for each of 152 SMs, so that each is one run of tiles
+    c = torch.cat([torch.zeros(128), torch.full((33000 + 300,), 7.875)]).cuda()
+    k = c[:, None, None].expand(-1, heads, dim)
+    v = randn(5, len(c), heads, dim) * size
+    v[:128 + 33000] = 0
+    cache, batch, kk, vv = one_sequence(at, k, v, dtype, copies=copies, new=new)
+    q = torch.ones(copies * new, heads, dim, dtype=BF16, device="cuda")
+    got = at.dflash2_paged_attention(q, cache, batch, scale=unit_scale(dim))
+    want, mag, lse = attend(q[:new], [kk], [vv], [len(c)], [new], unit_scale(dim), True, 0)
+    assert ((got["out"].double() - want.repeat(copies, 1, 1)).abs() <= attend_bound(want, mag).repeat(copies, 1, 1)).all()
+    assert lse_close(got["lse"], lse.repeat(copies, 1))
 
 
 # ------------------------------------------------------------------------------------------ waits
