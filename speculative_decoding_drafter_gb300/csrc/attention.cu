@@ -31,7 +31,7 @@
 // P is zero elsewhere), with its own m and l, and the copies are added up at the end of the item.
 // 8-bit caches: codes are exact in f16, so K's scale multiplies the score, and V's goes into the
 // exponent: x'_j = x_j + log2(vs_j), P'_j = 2^(x'_j - m'), o = sum P'_j code_j, l = sum P'_j / vs_j,
-// which keeps P' in f16's range whatever the values' size.  Queries go to f16 by a power of two per
+// which keeps P' in f16's range whatever the values' size (2^7 P' is what is rounded, see kAbove).  Queries go to f16 by a power of two per
 // row that brings the row's largest magnitude to 2^14..2^15 (smaller parts lose bits only below
 // 2^-24 of it).  With a bf16 cache everything stays bf16; P is rounded once, to bf16 or f16, as the
 // MMA's operand; scores, sums and o are float32.
@@ -72,6 +72,9 @@ constexpr int SEGMENTS = 4;  // segments that the walking warp may be ahead
 constexpr int MAX_SCALES = 4;
 constexpr float kLeastScale = -108.f;  // log2 of the least scale a cache holds, 1e-30 / 448
 constexpr float LAZY = 8.f;   // how far the running maximum may lag, in powers of two
+// An 8-bit cache's P' are f16 with the maximum at 2^7, so at most 2^15 while it lags: what is up to
+// 2^-32 of the maximum is not lost (at 1 it was 2^-25: 3% of a result over a million such keys).
+constexpr float kAbove = 7.f, kBelow = 0x1p-7f;
 
 struct SplitRecord {  // an item whose pieces the combine kernel joins
     int32_t valid, first_slot, c0, c1, kvh, tok0, ntok, pad;
@@ -832,7 +835,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         ks[i] = held ? ks[i] : 0.f;
                         vs[i] = held ? vs[i] : 1.f;
                         lv[i] = vs[i] > 0.f ? __log2f(vs[i]) : vs[i];
-                        rv[i] = __fdividef(1.f, vs[i]);
+                        rv[i] = __fdividef(kBelow, vs[i]);
                         if (held && vs[i] > 0.f)
                             top_lv = fmaxf(top_lv, lv[i]);
                         zero = zero || vs[i] == 0.f;
@@ -848,7 +851,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             if (vs[i] == 0.f)
-                                lv[i] = ref, rv[i] = exp2f(-ref);
+                                lv[i] = ref, rv[i] = kBelow * exp2f(-ref);
                     }
                     float4 *sm = reinterpret_cast<float4 *>(smem + lay.scales + tcnt % kScales * 3 * BN * 4) + lane;
                     sm[0] = make_float4(ks[0], ks[1], ks[2], ks[3]);
@@ -1101,7 +1104,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                             }
                             if (move)
                                 m = tile_top;
-                            const float base = m == -INFINITY ? 0.f : -m * sl2;
+                            const float base = m == -INFINITY ? 0.f : (kQuant ? kAbove : 0.f) - m * sl2;
                             const uint64_t base2 = f2(base, base), sl22 = f2(sl2, sl2);
                             uint64_t sum2[2] = {0, 0};
                             if constexpr (FOLD > 1) {  // the other copies' keys
@@ -1221,6 +1224,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
             if constexpr (kQuant) {
                 if (log_more > -INFINITY)
                     log_l = log_sum(log_l, log_more - m);
+                m -= kAbove, log_l += kAbove;  // o is in units of 2^(m - 7)
             }
             if constexpr (FOLD > 1) {
                 // the copies' common maximum; each copy's weight; the sum of their sums

@@ -5,11 +5,12 @@ import threading
 import pytest
 import torch
 
-from attention_rules import BF16, Batch, attend, attend_bound
+from attention_rules import BF16, EPS16, Batch, attend, attend_bound
 
 pytestmark = pytest.mark.gpu
 
 E4M3, INT8 = torch.float8_e4m3fn, torch.int8
+EPS_F16 = 2.0 ** -11  # half a unit in f16's last place, relative
 EIGHT_BITS = pytest.mark.parametrize("dtype", [E4M3, INT8])
 
 
@@ -99,6 +100,27 @@ def test_sum_over_many_rows_of_zeros(at, dtype, new, size):
     got = at.dflash2_paged_attention(q, cache, batch, scale=unit_scale(dim))
     want, mag, lse = attend(q[:new], [kk], [vv], [len(c)], [new], unit_scale(dim), True, 0)
     assert ((got["out"].double() - want.repeat(copies, 1, 1)).abs() <= attend_bound(want, mag).repeat(copies, 1, 1)).all()
+    assert lse_close(got["lse"], lse.repeat(copies, 1))
+
+
+@EIGHT_BITS
+@pytest.mark.parametrize("apart", [24.0, 26.0, 28.5])
+@pytest.mark.parametrize("new", [1, 40])
+def test_many_small_probabilities_beside_a_large_one(at, dtype, apart, new):
+    """Keys 2^-24 and less below one dominant key still add up."""
+    dim, n, copies = 64, 3000, 76  # an item for each of 152 SMs, so that each is one run of tiles
+    k = torch.zeros(n, 2, dim, device="cuda")
+    k[0] = apart
+    v = torch.zeros(n, 2, dim, device="cuda")
+    v[0, :, 0] = 1
+    v[1:, :, 1:] = 1
+    cache, batch, kk, vv = one_sequence(at, k, v, dtype, copies=copies, new=new)
+    q = torch.ones(copies * new, 8, dim, dtype=BF16, device="cuda")
+    got = at.dflash2_paged_attention(q, cache, batch, causal=False, scale=unit_scale(dim))
+    want, mag, lse = attend(q[:new], [kk], [vv], [n], [new], unit_scale(dim), False, 0)
+    # beside its relative rounding each probability has f16's absolute one, half of 2^-24 where the largest is 2^7
+    bound = EPS16 * want.abs() + (EPS_F16 + 2.0 ** -13) * mag + n * 2.0 ** -32
+    assert ((got["out"].double() - want.repeat(copies, 1, 1)).abs() <= bound.repeat(copies, 1, 1)).all()
     assert lse_close(got["lse"], lse.repeat(copies, 1))
 
 
