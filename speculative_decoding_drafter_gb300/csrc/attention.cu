@@ -534,7 +534,9 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     Segment next;
                     walk.next(a.work, sequence, cta, shares, next);
                     if (lane == 0) {
-                        segs[n % SEGMENTS] = next;
+                        if constexpr (kQuant)
+                        next.spoilt = 0;
+                    segs[n % SEGMENTS] = next;
                         mbar_arrive(seg_full(n % SEGMENTS));
                     }
                     __syncwarp();
@@ -804,6 +806,7 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 const Segment &g = segs[n % SEGMENTS];
                 const int tiles = g.tiles, lo = g.item.lo - g.tile * BN, hi = g.item.hi - g.tile * BN;
                 float top_lv = -INFINITY;  // this lane's largest log2 of a value scale in the segment
+                bool spoilt = false;
                 for (int j = 0; j < tiles; ++j) {
 #pragma unroll 1
                     while (asked - tcnt < kRaws && ask())
@@ -834,14 +837,17 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                         const bool held = k >= lo && k < hi;
                         ks[i] = held ? ks[i] : 0.f;
                         vs[i] = held ? vs[i] : 1.f;
-                        lv[i] = vs[i] > 0.f ? __log2f(vs[i]) : vs[i];
+                        if (!(vs[i] >= 0.f && vs[i] < INFINITY))
+                            vs[i] = 0.f, spoilt = true;
+                        lv[i] = __log2f(vs[i]);
                         rv[i] = __fdividef(kBelow, vs[i]);
                         if (held && vs[i] > 0.f)
                             top_lv = fmaxf(top_lv, lv[i]);
                         zero = zero || vs[i] == 0.f;
                     }
                     if (__any_sync(0xffffffffu, zero)) {
-                        // A row of zeros adds to l alone; any scale serves its codes.  One 2^60 below
+                        // A row of zeros adds to l alone (so does one that is not finite, whose rows of out
+                        // are made NaN at the end); any scale serves its codes.  One 2^60 below
                         // the largest seen keeps it from setting m' (P' of the others would fall out
                         // of f16) and its own P' far above float32's least.
                         float ref = top_lv;
@@ -857,6 +863,8 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                     sm[0] = make_float4(ks[0], ks[1], ks[2], ks[3]);
                     sm[BN / 4] = make_float4(lv[0], lv[1], lv[2], lv[3]);
                     sm[BN / 2] = make_float4(rv[0], rv[1], rv[2], rv[3]);
+                    if (spoilt)
+                        segs[n % SEGMENTS].spoilt = 1;
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(scale_full(tcnt % kScales));
@@ -1261,6 +1269,10 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                 else
                     inv = l > 0.f ? __fdividef(1.f, l) : l == 0.f ? 0.f : l;
             }
+            // a value row that is not finite is in out and not in the sum
+            const bool spoilt = kQuant && g.spoilt != 0 && log_l > -INFINITY;
+            if (spoilt)
+                inv = NAN;
             if (warp_live || FOLD > 1) {
                 constexpr int kChunk = FOLD > 1 ? 16 : 32;     // columns at a time
                 constexpr int kPer = kChunk / FOLD;            // ... of which this thread writes
@@ -1316,6 +1328,11 @@ __global__ void __launch_bounds__(Shape<QT, TYPE>::kThreads, 1)
                                 *reinterpret_cast<uint2 *>(to + 2 * k) = make_uint2(w[k], w[k + 1]);
                         }
                     } else if (live) {
+                        if (spoilt) {
+#pragma unroll
+                            for (int k = 0; k < kPer; ++k)
+                                o[k] = 0x7FC00000u;
+                        }
                         float *to = a.part_o + part * dim + c + k0;
                         if constexpr (kPer >= 8) {
 #pragma unroll

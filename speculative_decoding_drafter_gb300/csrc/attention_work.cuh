@@ -84,6 +84,7 @@ struct Segment {
     int first, last;     // has the item's first / last tile
     int slot;            // where a piece of an item goes
     int end_cta;         // of an item that begins here and ends elsewhere: the CTA with its last tile
+    int spoilt;          // a value row that its tiles hold is not finite (8-bit caches; set on the way)
 };
 
 DF2_WORK long long quotient(long long a, long long b)

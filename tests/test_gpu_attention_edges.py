@@ -11,6 +11,7 @@ pytestmark = pytest.mark.gpu
 
 E4M3, INT8 = torch.float8_e4m3fn, torch.int8
 EPS_F16 = 2.0 ** -11  # half a unit in f16's last place, relative
+TYPES = pytest.mark.parametrize("dtype", [BF16, E4M3, INT8])
 EIGHT_BITS = pytest.mark.parametrize("dtype", [E4M3, INT8])
 
 
@@ -122,6 +123,26 @@ def test_many_small_probabilities_beside_a_large_one(at, dtype, apart, new):
     bound = EPS16 * want.abs() + (EPS_F16 + 2.0 ** -13) * mag + n * 2.0 ** -32
     assert ((got["out"].double() - want.repeat(copies, 1, 1)).abs() <= bound.repeat(copies, 1, 1)).all()
     assert lse_close(got["lse"], lse.repeat(copies, 1))
+
+
+@TYPES
+@pytest.mark.parametrize("new", [2, 20, 100])
+@pytest.mark.parametrize("copies", [1, 80])  # items in pieces, and whole ones
+def test_lse_where_a_value_is_not_finite(at, dtype, new, copies):
+    """lse is a function of queries and keys: a value row that is not finite reaches out and not lse."""
+    dim, n = 64, 700
+    k, v = randn(1, n, 2, dim), randn(2, n, 2, dim)
+    at_value = n - 1 - new // 2
+    v[at_value, 0, 3] = math.inf
+    cache, batch, kk, _ = one_sequence(at, k, v, dtype, copies=copies, new=new)
+    q = randn(3, new, 8, dim).to(BF16).repeat(copies, 1, 1)
+    got = at.dflash2_paged_attention(q, cache, batch)
+    clean = torch.zeros_like(kk)
+    _, _, lse = attend(q[:new], [kk], [clean], [n], [new], dim ** -0.5, True, 0)
+    assert lse_close(got["lse"], lse.repeat(copies, 1))
+    sees = (n - new + torch.arange(new, device="cuda") >= at_value).repeat(copies)
+    assert not torch.isfinite(got["out"][sees][:, :4]).all(-1).any()
+    assert torch.isfinite(got["out"][:, 4:]).all()  # another cache head's rows
 
 
 # ------------------------------------------------------------------------------------------ waits
