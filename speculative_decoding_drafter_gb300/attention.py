@@ -84,7 +84,7 @@ class PagedCache:
         if quantised != (k_scale is not None) or quantised != (v_scale is not None):
             raise ValueError("8-bit caches have k_scale and v_scale, bfloat16 caches have none")
         shape = tuple(k.shape)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.k, self.v, self.k_scale, self.v_scale = self._keep = k, v, k_scale, v_scale
         self.args = CacheArgs(pages, page_size, heads, dim, CACHE_TYPES[k.dtype], _ptr(k, k.dtype, shape, "k"),
                               _ptr(v, k.dtype, shape, "v"), _ptr(k_scale, torch.float32, shape[:3], "k_scale"),
                               _ptr(v_scale, torch.float32, shape[:3], "v_scale"))
@@ -117,7 +117,7 @@ class TokenBatch:
         B = kv_len.shape[0] if kv_len.dim() else 0
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be an int32 tensor [B, max_pages]")
-        self.token_start, self.kv_len, self.page_table = token_start, kv_len, page_table
+        self.token_start, self.kv_len, self.page_table = self._keep = token_start, kv_len, page_table
         self.tokens = int(tokens)
         self.args = TokenArgs(B, self.tokens, self.tokens if max_new is None else int(max_new), page_table.shape[1],
                               _ptr(token_start, torch.int32, (B + 1,), "token_start"),
@@ -151,7 +151,8 @@ class AttentionWorkspace:
 
 class _Plan:
     """A C call with its arguments checked and bound.  Calling launches it on the stream the plan was
-    given, or else on the current stream of the call, and returns the bound outputs."""
+    given, or else on the current stream of the call, and returns the bound outputs (a dict of its own
+    each time).  What is bound stays so, and alive, whatever becomes of names and dicts around it."""
 
     _name = ""
 
@@ -159,6 +160,8 @@ class _Plan:
         self._fn = getattr(library(), self._name)
         self._device = torch.cuda.current_device()
         self._args, self._keep, self.outputs = args, keep, outputs
+        self._several = isinstance(outputs, dict)
+        self._bound = dict(outputs) if self._several else outputs
         self._handle = None if stream is None else _stream(stream)
 
     def __call__(self):
@@ -166,7 +169,7 @@ class _Plan:
         st = self._fn(*self._args, _current_stream(self._device) if handle is None else handle)
         if st:
             raise DFlash2Error(st, self._name)
-        return self.outputs
+        return self._bound.copy() if self._several else self._bound
 
 
 # the raw handle without building a stream object, which costs as much as the launch
@@ -275,7 +278,7 @@ class PagedAttentionPlan(_Plan):
         self.workspace = ws
         outputs = {"out": out} if lse is None else {"out": out, "lse": lse}
         self._bind((_ref(cache.args), _ref(batch.args), _ref(opts), _ref(qr), _ref(outr),
-                    _ptr(lse, torch.float32, (N, heads), "lse"), ws.ptr, ws.nbytes), (cache, batch, opts, qr, outr, q),
+                    _ptr(lse, torch.float32, (N, heads), "lse"), ws.ptr, ws.nbytes), (cache, batch, opts, qr, outr, q, ws),
                    outputs, stream)
 
 

@@ -82,6 +82,26 @@ def test_calls_of_several_sizes_from_two_threads(at):
     assert not failed
 
 
+def test_what_a_plan_binds_stays_bound(at):
+    """Emptying the dict that a call returned, or taking the names off a cache, a batch and a workspace, leaves the
+    next call's buffers alive and its results the same."""
+    k, v = randn(1, 300, 2, 128), randn(2, 300, 2, 128)
+    cache, batch, _, _ = one_sequence(at, k, v, E4M3, new=5)
+    q = randn(3, 5, 4, 128).to(BF16)
+    plan = at.PagedAttentionPlan(q, cache, batch)
+    first = plan()
+    want = {name: t.clone() for name, t in first.items()}
+    first.clear()
+    plan.outputs.clear()
+    plan.workspace = None
+    cache.k = cache.v = cache.k_scale = cache.v_scale = None
+    batch.token_start = batch.kv_len = batch.page_table = None
+    fill = [torch.full((1 << 16,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(64)]  # takes what was let go
+    again = plan()
+    assert set(again) == set(want) and all(torch.equal(again[name], want[name]) for name in want)
+    assert all((f == 0xFF).all() for f in fill)
+
+
 # ------------------------------------------------------------------------------------------ numbers
 
 
