@@ -35,6 +35,14 @@ def _ref(struct):
     return None if struct is None else ctypes.byref(struct)
 
 
+def _int32(value, name):
+    """A count as the C ABI takes it (ctypes would cut it to 32 bits without a word)."""
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _rows(t, N, heads, dim, name):
     """df2_heads of a bf16 tensor [N, heads, dim] whose last dimension is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -48,7 +56,7 @@ def _rows(t, N, heads, dim, name):
         raise ValueError(f"{name} must have shape {(N, heads, dim)}, got {tuple(t.shape)}")
     if t.numel() and t.stride(2) != 1 and dim > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return HeadRows(t.data_ptr(), heads, t.stride(0), t.stride(1))
+    return HeadRows(t.data_ptr(), _int32(heads, name + "'s heads"), t.stride(0), t.stride(1))
 
 
 def _heads_of(t, name):
@@ -65,7 +73,8 @@ def _table(table, interleaved):
     if not isinstance(table, torch.Tensor) or table.dim() != 3 or table.shape[1] != 2:
         raise ValueError("table must be a float32 tensor [max_pos, 2, rot / 2]")
     shape = tuple(table.shape)
-    return RopeArgs(_ptr(table, torch.float32, shape, "table"), shape[0], 2 * shape[2], int(bool(interleaved)))
+    return RopeArgs(_ptr(table, torch.float32, shape, "table"), _int32(shape[0], "max_pos"),
+                    _int32(2 * shape[2], "rot"), int(bool(interleaved)))
 
 
 class PagedCache:
@@ -79,12 +88,12 @@ class PagedCache:
             raise TypeError(f"k must be one of {[str(t) for t in CACHE_TYPES]}, got {k.dtype}")
         if k.dim() != 4:
             raise ValueError(f"k must have shape [pages, heads, page_size, dim], got {tuple(k.shape)}")
-        pages, heads, page_size, dim = k.shape
         quantised = k.dtype != torch.bfloat16
         if quantised != (k_scale is not None) or quantised != (v_scale is not None):
             raise ValueError("8-bit caches have k_scale and v_scale, bfloat16 caches have none")
         shape = tuple(k.shape)
         self.k, self.v, self.k_scale, self.v_scale = self._keep = k, v, k_scale, v_scale
+        pages, heads, page_size, dim = (_int32(n, name) for n, name in zip(shape, ("pages", "heads", "page_size", "dim")))
         self.args = CacheArgs(pages, page_size, heads, dim, CACHE_TYPES[k.dtype], _ptr(k, k.dtype, shape, "k"),
                               _ptr(v, k.dtype, shape, "v"), _ptr(k_scale, torch.float32, shape[:3], "k_scale"),
                               _ptr(v_scale, torch.float32, shape[:3], "v_scale"))
@@ -118,8 +127,10 @@ class TokenBatch:
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table must be an int32 tensor [B, max_pages]")
         self.token_start, self.kv_len, self.page_table = self._keep = token_start, kv_len, page_table
-        self.tokens = int(tokens)
-        self.args = TokenArgs(B, self.tokens, self.tokens if max_new is None else int(max_new), page_table.shape[1],
+        self.tokens = _int32(tokens, "tokens")
+        self.args = TokenArgs(_int32(B, "sequences"), self.tokens,
+                              self.tokens if max_new is None else _int32(max_new, "max_new"),
+                              _int32(page_table.shape[1], "max_pages"),
                               _ptr(token_start, torch.int32, (B + 1,), "token_start"),
                               _ptr(kv_len, torch.int32, (B,), "kv_len"),
                               _ptr(page_table, torch.int32, (B, page_table.shape[1]), "page_table"))
@@ -127,7 +138,7 @@ class TokenBatch:
 
 def dflash2_paged_attention_workspace_bytes(cache: PagedCache, batch: TokenBatch, q_heads: int) -> int:
     return int(library().dflash2_paged_attention_workspace_bytes(ctypes.byref(cache.args), ctypes.byref(batch.args),
-                                                                 int(q_heads)))
+                                                                 _int32(q_heads, "q_heads")))
 
 
 class AttentionWorkspace:
@@ -198,7 +209,7 @@ class RopePlan(_Plan):
             raise ValueError("table must be a float32 tensor [max_pos, 2, rot / 2]")
         out = _out_like(x) if out is None else out
         yr = _rows(out, N, heads, dim, "out")
-        self._bind((_ref(rope), N, dim, _ref(xr), pos, int(bool(inverse)), _ref(yr)),
+        self._bind((_ref(rope), _int32(N, "tokens"), _int32(dim, "dim"), _ref(xr), pos, int(bool(inverse)), _ref(yr)),
                    (rope, xr, yr, x, positions, table), out, stream)
 
 
@@ -267,7 +278,8 @@ class PagedAttentionPlan(_Plan):
             lse = torch.empty((N, heads), dtype=torch.float32, device=q.device)
         elif lse is False:
             lse = None
-        opts = AttentionArgs(dim ** -0.5 if scale is None else float(scale), int(bool(causal)), int(window))
+        opts = AttentionArgs(dim ** -0.5 if scale is None else float(scale), int(bool(causal)),
+                             _int32(min(int(window), 2 ** 31 - 1), "window"))  # past every position: no limit
         if not math.isfinite(opts.scale):
             raise ValueError("scale must be finite")
         ws = workspace
@@ -290,12 +302,13 @@ def dflash2_rope_table(max_pos: int, rot: int, *, theta: float = 10000.0, kind: 
     "linear", "base", "ramp", "band" (df2_rope_kind), the latter four stretched by `factor`."""
     if kind not in ROPE_KINDS:
         raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}, got {kind!r}")
+    max_pos, rot = _int32(max_pos, "max_pos"), _int32(rot, "rot")
     if out is None:
         if max_pos < 1 or rot < 2 or rot % 2:
             raise ValueError("max_pos must be positive and rot even and positive")
         out = torch.empty((max_pos, 2, rot // 2), dtype=torch.float32, device="cuda")
     s = RopeScaling(ROPE_KINDS[kind], theta, factor, original_len, low, high, multiplier)
-    st = library().dflash2_rope_table(ctypes.byref(s), int(max_pos), int(rot),
+    st = library().dflash2_rope_table(ctypes.byref(s), max_pos, rot,
                                       _ptr(out, torch.float32, (max_pos, 2, rot // 2), "out"), _stream(stream))
     _check(st, "dflash2_rope_table")
     return out

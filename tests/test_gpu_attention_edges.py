@@ -102,6 +102,20 @@ def test_what_a_plan_binds_stays_bound(at):
     assert all((f == 0xFF).all() for f in fill)
 
 
+def test_counts_that_32_bits_do_not_hold(at):
+    """A window past every position is no limit, not what is left of it in 32 bits; other counts are refused."""
+    k, v = randn(1, 300, 2, 64), randn(2, 300, 2, 64)
+    cache, batch, _, _ = one_sequence(at, k, v, BF16, new=5)
+    q = randn(3, 5, 4, 64).to(BF16)
+    want = at.dflash2_paged_attention(q, cache, batch)
+    for window in (2 ** 31 - 1, 2 ** 32 + 1, 10 ** 12):
+        got = at.dflash2_paged_attention(q, cache, batch, window=window)
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    for kw in (dict(tokens=5, max_new=2 ** 32 + 1), dict(tokens=2 ** 32 + 5)):
+        with pytest.raises(ValueError, match="must fit 32 bits"):
+            at.TokenBatch(batch.token_start, batch.kv_len, batch.page_table, **kw)
+
+
 # ------------------------------------------------------------------------------------------ numbers
 
 
