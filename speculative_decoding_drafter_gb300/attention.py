@@ -118,7 +118,10 @@ class PagedCache:
 
 class TokenBatch:
     """The new tokens of a batch of sequences: token_start int32 [B + 1], kv_len int32 [B] (new tokens
-    included), page_table int32 [B, max_pages]; tokens = token_start[B], no sequence has more than max_new."""
+    included), page_table int32 [B, max_pages]; tokens = token_start[B], no sequence has more than max_new.
+    max_new may be larger than tokens (a loop's block length, a short last batch).  It sets how many rows
+    attention plans for: give it where sequences have few tokens each, it is taken as `tokens` if not given
+    (64 sequences of one token are then planned as one of 64: the same results, slower)."""
 
     def __init__(self, token_start, kv_len, page_table, *, tokens: int, max_new: int | None = None):
         if not isinstance(kv_len, torch.Tensor) or not kv_len.is_cuda:
@@ -128,8 +131,8 @@ class TokenBatch:
             raise ValueError("page_table must be an int32 tensor [B, max_pages]")
         self.token_start, self.kv_len, self.page_table = self._keep = token_start, kv_len, page_table
         self.tokens = _int32(tokens, "tokens")
-        self.args = TokenArgs(_int32(B, "sequences"), self.tokens,
-                              self.tokens if max_new is None else _int32(max_new, "max_new"),
+        max_new = self.tokens if max_new is None else min(_int32(max_new, "max_new"), self.tokens)
+        self.args = TokenArgs(_int32(B, "sequences"), self.tokens, max_new,
                               _int32(page_table.shape[1], "max_pages"),
                               _ptr(token_start, torch.int32, (B + 1,), "token_start"),
                               _ptr(kv_len, torch.int32, (B,), "kv_len"),

@@ -116,6 +116,21 @@ def test_counts_that_32_bits_do_not_hold(at):
             at.TokenBatch(batch.token_start, batch.kv_len, batch.page_table, **kw)
 
 
+@pytest.mark.parametrize("new", [0, 1, 3])
+def test_a_batch_shorter_than_its_block_length(at, new):
+    """max_new bound once to a loop's block length, and a last batch with fewer tokens in all."""
+    k, v = randn(1, 300, 2, 64), randn(2, 300, 2, 64)
+    cache, batch, kk, vv = one_sequence(at, k, v, E4M3, new=new)
+    short = at.TokenBatch(batch.token_start, batch.kv_len, batch.page_table, tokens=new, max_new=16)
+    q = randn(3, new, 4, 64).to(BF16)
+    got = at.dflash2_paged_attention(q, cache, short)
+    want, mag, lse = attend(q, [kk], [vv], [300], [new], 64 ** -0.5, True, 0)
+    assert ((got["out"].double() - want).abs() <= attend_bound(want, mag)).all() and lse_close(got["lse"], lse)
+    read, both = at.dflash2_cache_read(cache, short), at.dflash2_cache_read(cache, batch)
+    assert torch.equal(read["k"], both["k"]) and torch.equal(read["v"], both["v"])
+    at.dflash2_cache_append(cache, short, both["k"], both["v"])
+
+
 # ------------------------------------------------------------------------------------------ numbers
 
 
