@@ -367,7 +367,8 @@ typedef struct df2_cache {
  *   token_start int32 [B + 1], rising from 0 to N;  kv_len int32 [B];
  *   page_table int32 [B, max_pages]: only the entries of positions that a call touches are used.
  * max_new: no n_b is larger; 1 <= max_new <= N (0 if N is 0; a caller with a fixed block length
- * passes the smaller of it and N).  B <= 2048, max_pages * page_size <= 2^30.  A row whose
+ * passes the smaller of it and N); it sets how rows are laid out over tiles, and attention to
+ * a sequence with more is only slower.  B <= 2048, max_pages * page_size <= 2^30.  A row whose
  * position is negative (kv_len[b] < n_b) is padding: it is not written, reads back as zeros, and
  * with causal attention sees nothing.  Page ids outside
  * [0, pages) and positions past max_pages * page_size are the caller's mistake: they are not

@@ -1655,7 +1655,8 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     const int tiles = row_tiles(tokens, a.group);
     const int fold = row_copies(cache, tokens, a.group);
     a.tpm = BM / fold / a.group;
-    a.work.span = tiles * a.tpm;
+    // no item has more rows than the combine kernel looks at, even where a sequence has more than max_new
+    a.work.span = tiles == 2 ? 2 * a.tpm : std::min(a.tpm, tokens.max_new);
     a.work.heads = cache.heads;
     // Measured on GB300: 2048 tokens over their own 2048 keys (two row tiles) 100.7, 84.4, 76.5, 73.2,
     // 70.5 and 71.4 us at 0, 1, 2, 3, 4 and 6; 7 blocks of 16 over 1000 keys (one) 20.3, 17.4 and
@@ -1679,7 +1680,7 @@ cudaError_t launch_paged_attention(const PagedCache &cache, const TokenBatch &to
     if (e != cudaSuccess)
         return e;
     // the rows that an item can have, eight to a CTA
-    const long long most = tiles == 2 ? 2 * BM : std::min<long long>(a.tpm, tokens.max_new) * a.group;
+    const int most = tiles == 2 ? 2 * BM : a.work.span * a.group;
     const unsigned y = static_cast<unsigned>((most + 7) / 8);
     return launch_dependent(combine_kernel, dim3(static_cast<unsigned>(sms), y), dim3(256), 0, stream, a, tiles * BM);
 }

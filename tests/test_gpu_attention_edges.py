@@ -131,6 +131,21 @@ def test_a_batch_shorter_than_its_block_length(at, new):
     at.dflash2_cache_append(cache, short, both["k"], both["v"])
 
 
+@TYPES
+@pytest.mark.parametrize("new", [5, 70])
+def test_a_sequence_with_more_tokens_than_said(at, dtype, new):
+    """Every row is there, also where its item is worked on by several SMs."""
+    k, v = randn(1, 5000, 2, 64), randn(2, 5000, 2, 64)
+    cache, batch, kk, vv = one_sequence(at, k, v, dtype, copies=3, new=new)
+    wrong = at.TokenBatch(batch.token_start, batch.kv_len, batch.page_table, tokens=3 * new, max_new=1)
+    q = randn(3, new, 4, 64).to(BF16).repeat(3, 1, 1)
+    out, lse_out = torch.full_like(q, math.nan), torch.full((3 * new, 4), math.nan, device="cuda")
+    got = at.dflash2_paged_attention(q, cache, wrong, out=out, lse=lse_out)
+    want, mag, lse = attend(q[:new], [kk], [vv], [5000], [new], 64 ** -0.5, True, 0)
+    assert ((got["out"].double() - want.repeat(3, 1, 1)).abs() <= attend_bound(want, mag).repeat(3, 1, 1)).all()
+    assert lse_close(got["lse"], lse.repeat(3, 1))
+
+
 # ------------------------------------------------------------------------------------------ numbers
 
 
