@@ -10,10 +10,10 @@
 // in place of a division changes a code only where x M / m is within 2 ulp of a rounding boundary.
 //
 // Both kernels only move data: 2 bytes in and 2 (bf16) or 1 (8-bit) out per element, a few
-// operations each, so HBM bounds long calls and latency short ones.  A row is at most 256 bytes:
-// 16 lanes hold one (8 elements, 16 bytes a lane), a warp works on rows of one token, so the
-// sequence lookup, the page lookup and the cosines and sines in registers serve all of its rows,
-// and every pair's partner is in the lane itself or one shuffle away.
+// operations each, so HBM bounds long calls and latency short ones.  A row is at most 256 bytes (512
+// where it is only rotated): 16 (32) lanes hold one, 8 elements or 16 bytes a lane.  A warp works on
+// rows of one token, so the sequence lookup, the page lookup and the cosines and sines in registers
+// serve all of its rows, and every pair's partner is in the lane itself or one shuffle away.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const RowsArgs a)
 // Many tokens: a warp takes all rows of `run` tokens in a row, the next R rows a lane on their way
 // while R are worked on.  The tokens' places are looked up at once, a lane each, and the next
 // token's cosines and sines are asked for when only values, which do not turn, are left of this one.
+// At the 64 registers that four CTAs an SM leave, a thread spills 40 to 64 bytes.
 template <int LG, int R, bool CACHE>
 __global__ void __launch_bounds__(kThreads, 4) rows_run_kernel(const RowsArgs a, int run)
 {
@@ -470,12 +471,6 @@ cudaError_t launch_rows(RowsArgs a, cudaStream_t stream)
     return launch_dependent(rows_run_kernel<LG, 2, CACHE>, dim3(grid), dim3(kThreads), 0, stream, a, run);
 }
 
-template <bool CACHE>
-cudaError_t launch_rows(const RowsArgs &a, cudaStream_t stream)
-{
-    return a.dim > 128 ? launch_rows<32, CACHE>(a, stream) : launch_rows<16, CACHE>(a, stream);
-}
-
 }  // namespace
 
 cudaError_t launch_rope_table(const RopeScaling &s, int max_pos, int rot, float *table, cudaStream_t stream)
@@ -497,7 +492,7 @@ cudaError_t launch_rope(const RopeTable &rope, int N, int dim, const HeadRows &x
     a.dim = dim;
     a.sine_sign = sine_sign;
     a.rows = x.heads;
-    return launch_rows<false>(a, stream);
+    return dim > 128 ? launch_rows<32, false>(a, stream) : launch_rows<16, false>(a, stream);
 }
 
 cudaError_t launch_cache_append(const PagedCache &cache, const TokenBatch &tokens, const RopeTable &rope,
@@ -516,7 +511,7 @@ cudaError_t launch_cache_append(const PagedCache &cache, const TokenBatch &token
     a.dim = cache.dim;
     a.sine_sign = 1.f;
     a.rows = q.heads + 2 * cache.heads;
-    return launch_rows<true>(a, stream);
+    return launch_rows<16, true>(a, stream);  // a cache's dim is at most 128
 }
 
 cudaError_t launch_cache_read(const PagedCache &cache, const TokenBatch &tokens, const HeadRows &k_out,
