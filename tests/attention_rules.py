@@ -8,6 +8,7 @@ BF16 = torch.bfloat16
 TOP = {torch.float8_e4m3fn: 448.0, torch.int8: 127.0}
 EPS32 = 2.0 ** -24  # half a unit in the last place of float32, relative
 EPS16 = 2.0 ** -8   # ... of bfloat16 (8 significand bits)
+EPS_F16 = 2.0 ** -11  # ... of float16 (11)
 
 
 def rotate(x, table, positions, interleaved, inverse=False):
@@ -122,3 +123,17 @@ def attend_bound(out, mag):
     (relative 2^-8, so at most 2^-8 sum p |v| in all); scores and sums in float32 (2^-13 of sum p |v|
     allows a score error of 2^-14, 128 terms of 2^-24 times scores up to 8)."""
     return EPS16 * out.abs() + (EPS16 + 2.0 ** -13) * mag + 1e-30
+
+
+def tile_values(n, heads, dim, device="cuda"):
+    """Value rows of one 1: channel d is that of the key tiles t with t mod dim == d, so that it counts them."""
+    v = torch.zeros(n, heads, dim, device=device)
+    p = torch.arange(n, device=device)
+    v[p, :, (p // 128) % dim] = 1
+    return v
+
+
+def tile_bound(want, squares, eps_p):
+    """For such values: a result's rounding to bfloat16; each probability rounded to nearest, independently (seven times
+    the root of the sum of squares: 1e-10 that a result passes it); float32 sums of positive terms."""
+    return EPS16 * want.abs() + 7 * eps_p * squares.sqrt() + 2.0 ** -13 * want.abs()

@@ -5,12 +5,12 @@ import threading
 import pytest
 import torch
 
-from attention_rules import BF16, EPS16, Batch, attend, attend_bound
+from attention_rules import BF16, EPS16, EPS_F16, Batch, attend, attend_bound, tile_bound, tile_values
+from test_gpu_attention import check
 
 pytestmark = pytest.mark.gpu
 
 E4M3, INT8 = torch.float8_e4m3fn, torch.int8
-EPS_F16 = 2.0 ** -11  # half a unit in f16's last place, relative
 TYPES = pytest.mark.parametrize("dtype", [BF16, E4M3, INT8])
 EIGHT_BITS = pytest.mark.parametrize("dtype", [E4M3, INT8])
 
@@ -207,6 +207,45 @@ def test_lse_where_a_value_is_not_finite(at, dtype, new, copies):
     sees = (n - new + torch.arange(new, device="cuda") >= at_value).repeat(copies)
     assert not torch.isfinite(got["out"][sees][:, :4]).all(-1).any()
     assert torch.isfinite(got["out"][:, 4:]).all()  # another cache head's rows
+
+
+# ------------------------------------------------------------------------------------------ every tile
+
+
+@TYPES
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+@pytest.mark.parametrize("lens,new", [([163000], 2), ([163000], 40), ([9000 - 211 * i for i in range(40)], 1),
+                                      ([9000 - 211 * i for i in range(40)], 40), ([50000, 20, 7], 100)])
+def test_every_tile_is_in_the_result(at, dtype, spread, lens, new):
+    """Channels that count tiles: one tile's products lost, or taken twice, is an error of 1 / 20 and more."""
+    heads, dim, n = 2, 64, max(lens)
+    k = randn(1, n, heads, dim)
+    cache, batch, kk, vv = one_sequence(at, k, tile_values(n, heads, dim), dtype, copies=len(lens), new=new)
+    batch.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+    q = (spread * randn(2, len(lens) * new, 4, dim)).to(BF16)
+    got = at.dflash2_paged_attention(q, cache, batch, causal=False)
+    group = 4 // heads
+    for b, length in enumerate(lens):
+        rows = slice(b * new, (b + 1) * new)  # positions below zero are padding, which sees the keys there are
+        want, _, lse = attend(q[rows], [kk[:length]], [vv[:length]], [length], [new], dim ** -0.5, False, 0)
+        s = torch.einsum("thd,jhd->thj", q[rows].double(), kk[:length].repeat_interleave(group, 1)) * dim ** -0.5
+        p = torch.exp(s - lse[..., None])
+        squares = torch.einsum("thj,jhd->thd", p * p, vv[:length].repeat_interleave(group, 1))
+        bound = tile_bound(want, squares, EPS16 if dtype == BF16 else EPS_F16)
+        assert ((got["out"][rows].double() - want).abs() <= bound).all()
+        assert lse_close(got["lse"][rows], lse)
+
+
+@TYPES
+@pytest.mark.parametrize("most,dim", [(3, 64), (3, 128), (45, 64), (45, 128)])
+def test_as_many_sequences_as_there_may_be(at, dtype, most, dim):
+    """2048 sequences, many of them empty or without new tokens, in one row tile and in two."""
+    lens = [(37 * i) % 211 for i in range(2048)]
+    lens[-40:] = [0] * 40
+    news = [min(n, i % 4) for i, n in enumerate(lens)]
+    for i in range(3, 2000, 250):
+        news[i] = min(lens[i], most)
+    check(at, lens, news, 16, 4, 1, dim, dtype, True, 0, seed=dim + most)
 
 
 # ------------------------------------------------------------------------------------------ waits
