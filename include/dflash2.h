@@ -352,7 +352,9 @@ typedef enum df2_cache_type { DF2_CACHE_BF16 = 0, DF2_CACHE_E4M3 = 1, DF2_CACHE_
  * A row (one token, one head) is held as codes times its scale:
  *   m = max |row|,  scale = m / M,  code = round(row * (M / m)),  M = 448 (e4m3) or 127 (int8),
  * each operation in float32, codes rounded to nearest even.  A row with m < 1e-30 is held as
- * zeros; one that is not finite gets a NaN scale and reads back as NaN throughout.
+ * zeros; one that is not finite gets a NaN scale and reads back as NaN throughout.  (So scales are
+ * 0, at least 1e-30 / M, or NaN; attention counts on it in a cache that a caller fills itself, and
+ * takes a row with a negative or infinite scale as one that is not finite.)
  * page_size a multiple of 8 up to 1024; dim a multiple of 16 up to 128; 1 <= heads <= 1024. */
 typedef struct df2_cache {
     int32_t pages, page_size, heads, dim, type;
@@ -413,7 +415,15 @@ DF2_API size_t dflash2_paged_attention_workspace_bytes(const df2_cache *cache, c
  * of the exponentials.  A row that sees nothing gets zeros and -inf.
  * What the cache and the page table hold for positions that no row of a sequence sees may be
  * anything (a last page's tail, pages given back below a window).  A key that is not finite
- * reaches the rows that see it; a value that is not finite may reach every row of its sequence.
+ * reaches the rows that see it; a value that is not finite may reach every row of its sequence in
+ * out, and none in lse.
+ * Scores, sums and out are float32 until out is rounded.  Rounded before: probabilities to bf16, as
+ * operands of the product with the values (2^-8 of each; lse is not affected).  With an 8-bit cache
+ * instead probabilities times their values' scales to f16 (2^-11 of each; below 2^-32 of the row's
+ * largest they are lost to out), and queries to f16 after scaling by a power of two (a part below
+ * 2^-24 of its row's largest loses bits).  There the value rows that a row sees must not differ by
+ * more than a factor 2^100 in size, zeros apart: keys whose values lie further below the largest
+ * drop out of the sum of the exponentials.
  * q heads a multiple of cache heads, at most 64 times as many; N * q heads < 2^31. */
 DF2_API df2_status dflash2_paged_attention(const df2_cache *cache, const df2_tokens *tokens,
                                            const df2_attention *options, const df2_heads *q, const df2_heads *out,

@@ -209,6 +209,26 @@ def test_lse_where_a_value_is_not_finite(at, dtype, new, copies):
     assert torch.isfinite(got["out"][:, 4:]).all()  # another cache head's rows
 
 
+@TYPES
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling"])
+@pytest.mark.parametrize("new", [3, 100])
+def test_values_of_very_different_size_side_by_side(at, dtype, order, new):
+    """Value rows 2^100 apart, and rows of zeros: each key counts in the sum of the exponentials whatever its value."""
+    dim, n = 64, 2500
+    power = torch.linspace(-50, 50, n, device="cuda").round()
+    power = {"mixed": power[torch.randperm(n, generator=torch.Generator().manual_seed(1)).cuda()], "rising": power,
+             "falling": power.flip(0)}[order]
+    k = randn(1, n, 2, dim)
+    v = randn(2, n, 2, dim) * torch.exp2(power)[:, None, None]
+    v[::7] = 0
+    cache, batch, kk, vv = one_sequence(at, k, v, dtype, copies=76, new=new)
+    q = randn(3, new, 8, dim).to(BF16)
+    got = at.dflash2_paged_attention(q.repeat(76, 1, 1), cache, batch)
+    want, mag, lse = attend(q, [kk], [vv], [n], [new], dim ** -0.5, True, 0)
+    assert ((got["out"].double() - want.repeat(76, 1, 1)).abs() <= attend_bound(want, mag).repeat(76, 1, 1)).all()
+    assert lse_close(got["lse"], lse.repeat(76, 1))
+
+
 # ------------------------------------------------------------------------------------------ every tile
 
 
