@@ -31,19 +31,22 @@
 // P is zero elsewhere), with its own m and l, and the copies are added up at the end of the item.
 // 8-bit caches: codes are exact in f16, so K's scale multiplies the score, and V's goes into the
 // exponent: x'_j = x_j + log2(vs_j), P'_j = 2^(x'_j - m'), o = sum P'_j code_j, l = sum P'_j / vs_j,
-// which keeps P' in f16's range whatever the values' size (2^7 P' is what is rounded, see kAbove).  Queries go to f16 by a power of two per
+// which keeps P' in f16's range whatever the values' size (2^7 P' is what is rounded, see kAbove).
+// Value rows of zeros, and those that are not finite, get a scale that leaves m' to the others; the
+// latter mark their run of tiles, whose rows of o end as NaN.  Queries go to f16 by a power of two per
 // row that brings the row's largest magnitude to 2^14..2^15 (smaller parts lose bits only below
 // 2^-24 of it).  With a bf16 cache everything stays bf16; P is rounded once, to bf16 or f16, as the
 // MMA's operand; scores, sums and o are float32.
 //
 // What bounds it, and measured on one GB300 (copy 6768 GB/s, cuBLAS bf16 1957 TFLOP/s burst):
-//   32 sequences x 16 tokens, up to 8192 keys, 32 / 8 heads of 128, bf16: HBM; 132 us, 5.9 TB/s
-//     (the kernel alone 124 us and 1.01 times the algorithmic bytes; the rest is the combine kernel)
+//   32 sequences x 16 tokens, up to 8192 keys, 32 / 8 heads of 128, bf16: HBM; 131 us, 5.9 TB/s
+//     (the kernel alone 126 us and 1.01 times the algorithmic bytes; the rest is the combine kernel)
 //   32 x 8 tokens, up to 16384 keys, e4m3: shared memory, which the codes cross three times (TMA in,
-//     widening, MMA); 170 to 179 us, 4.4 to 4.7 TB/s
+//     widening, MMA: some 1,540 of the 2,190 cycles of a tile); 171 to 177 us, 4.5 to 4.6 TB/s
 //   one sequence, 2048 tokens over 18432 keys, bf16: the chain of a tile's softmax and products;
-//     383 us cold, 1.52 PFLOP/s, 397 to 425 back to back under the power cap
-//   one token over 777 keys: a chain of latencies (lengths, pages, tile, softmax, combine); 9.7 us
+//     373 us cold, 1.57 PFLOP/s, 382 to 406 back to back under the power cap; over e4m3 661 to 672,
+//     every CTA widening each key tile again for its own 256 rows
+//   one token over 777 keys: a chain of latencies (lengths, pages, tile, softmax, combine); 9.8 to 10.3 us
 // The code of all roles has to fit the instruction cache: with the walk in every role and loops
 // unrolled (11,200 instructions) warps waited for instructions and the e4m3 case took 330 us.
 #include <cuda_runtime.h>
