@@ -64,11 +64,10 @@ def draw(rng):
             case["out"] = rng.choice(["bf16", "e4m3", "both"])
         return case
     if op == "clip":
-        write = rng.random() < 0.7
-        tensors = _log(rng, 1, 60 if write else 800)  # each written one is an output of its own
+        tensors = _log(rng, 1, 800)
         return {"op": op, "tensors": tensors, "total": _log(rng, max(1000, 4 * tensors), 600000000),
                 "type": rng.choice(["bf16", "fp16", "fp32", "mixed"]), "kind": rng.choice(["l2", "l2", "max"]),
-                "write": write}
+                "write": rng.random() < 0.7}
     dim = 8 * _log(rng, 8, 672)
     vocab = _log(rng, 500, 262144)
     rows = _log(rng, 1, 4096)
