@@ -517,7 +517,7 @@ DF2_API df2_status dflash2_lm_head_loss(const df2_loss_dims *dims, const void *h
  *   dz_rv = (exp(z_rv - lse_r) - [v = label_r]) grad_r,  0 in ignored rows
  *   d_hidden bf16 [N, H] = dz . W_vocab   or NULL
  *   d_W      [V, H] = dz^T . hidden, of type d_W_type (DF2_BF16 or DF2_F32), or NULL; at least one of the two
- * The vocabulary is taken in pieces: the logits of a piece are made again, dz of the piece is rounded to bf16
+ * The vocabulary is taken in pieces: the logits of a piece are made again, the same bits as the loss's, dz of the piece is rounded to bf16
  * (2^-8 of each at most, as operand of both products; up to 128 rows to the sum of two bf16, 2^-16) and
  * multiplied; sums are float32 and d_hidden and d_W are rounded once.  What an ignored row holds (NaN too) reaches neither; its d_hidden is 0.
  * A row whose lse, grad or hidden is not finite reaches its own d_hidden and all of d_W.

@@ -61,7 +61,7 @@ constexpr int kStageK = 2 * kBlock;               // elements of K a stage
 constexpr int kStage = 4 * kBox;                  // A's two blocks, B's two blocks
 constexpr int kStages = 3;
 constexpr long long kSpread = 128 << 10, kSpreadFrom = 64 << 20;  // bytes of few rows' copies, and of W that make them
-constexpr int kGroup = 6;                         // stages of the loss's logits that one accumulator sums at most
+constexpr int kGroup = 6;                         // stages of a logit that one accumulator sums at most
 constexpr int kBufs = 2;                          // accumulators
 constexpr int kEpilogue = 8;                      // warps of the epilogue: 32 rows and half of the columns each
 constexpr int kCols = kTile / 2;                  // of a warp
@@ -332,7 +332,10 @@ __device__ __forceinline__ void stage_row(uint32_t buf, int lane, const uint32_t
 // Logits of many products: the stages are cut into even groups, whose sums the epilogue adds up rounded to nearest.  An
 // accumulator cuts off what does not fit (256 times for 4096 products: lse is then off by 1.8e-6 of it).  Groups of at most
 // 6 stages leave 5.7e-7 in the worst of a dozen sizes, of 14 1.4e-6, of 4 3.9e-7; 1024 x 5376 x 262144 takes 1484 us with
-// 6, 1486 to 1500 with 14, 1495 with 4; 1003 x 1024 x 50021 66.2, 65.9, 66.5.
+// 6, 1486 to 1500 with 14, 1495 with 4; 1003 x 1024 x 50021 66.2, 65.9, 66.5.  The gradient's logits are the same sums, bit by
+// bit: what a label's logit is off by is then in its row's lse too, and 1 - p of a row that is nearly fitted keeps its value
+// (1 - p near 1e-5, H = 4096: d_hidden off by 5% in the median, 20% and up to 47 times with all of H in one accumulator, which
+// cuts off more than lse's groups did; 64 x 5120 x 152064 takes 818 us and 816).
 __device__ __forceinline__ int group_of(int stages)
 {
     const int groups = (stages + kGroup - 1) / kGroup;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + static_cast<uint32_t>(buf * kTile);
-                    const int first = s, last = MODE == kLoss ? min(t.stages, s + group) : t.stages;
+                    const int first = s, last = MODE != kGrad ? min(t.stages, s + group) : t.stages;
                     for (; s < last; ++s) {
                         if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
                             ok = false;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (row_first >= (MODE != kGrad ? args.N : t.product == kHiddenGrad ? a.N : a.V - a.v0)) {
                 release();
                 bool there = true;
-                if (MODE == kLoss)
+                if (MODE != kGrad)
                     for (int s = group_of(t.stages); s < t.stages && (there = await()); s += group_of(t.stages))
                         release();
                 if (!there)
@@ -622,6 +625,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t = after;
                 continue;
             }
+            // The logits of a tile of several groups (this one's accumulator is the first's): their sums, block by block, to f.
+            // False if an accumulator does not come.
+            auto for_groups = [&](auto f) {
+                uint32_t sum[kCols / 32][32] = {};
+                const int group = group_of(t.stages);
+                for (int s = 0; s < t.stages; s += group) {
+                    if (s && !await())
+                        return false;
+#pragma unroll
+                    for (int cb = 0; cb < kCols / 32; ++cb) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(acc + cb * 32, r);
+                        tmem_wait_ld(r);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            sum[cb][j] = __float_as_uint(__uint_as_float(sum[cb][j]) + __uint_as_float(r[j]));
+                    }
+                    release();
+                }
+#pragma unroll
+                for (int cb = 0; cb < kCols / 32; ++cb)
+                    f(sum[cb], cb);
+                return true;
+            };
             const int n_first = t.n0 + first_col;
             const int col0 = a.v0 + n_first;  // MODE != kGrad: the first token
             if constexpr (MODE == kLoss) {
@@ -643,32 +670,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     run.add(r);
                 };
-                const int group = group_of(t.stages);
-                if (group == t.stages) {
+                if (group_of(t.stages) == t.stages)
                     for_blocks_once(acc, release, take);
-                } else {
-                    uint32_t sum[kCols / 32][32] = {};
-                    bool there = true;
-                    for (int s = 0; s < t.stages; s += group) {
-                        if (s && !(there = await()))
-                            break;
-#pragma unroll
-                        for (int cb = 0; cb < kCols / 32; ++cb) {
-                            uint32_t r[32];
-                            tmem_ld_32x32b_x32(acc + cb * 32, r);
-                            tmem_wait_ld(r);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                sum[cb][j] = __float_as_uint(__uint_as_float(sum[cb][j]) + __uint_as_float(r[j]));
-                        }
-                        release();
-                    }
-                    if (!there)
-                        break;
-#pragma unroll
-                    for (int cb = 0; cb < kCols / 32; ++cb)
-                        take(sum[cb], cb);
-                }
+                else if (!for_groups(take))
+                    break;
                 if (m < a.N)
                     a.part[static_cast<long long>(n_first / kCols) * a.N + m] = make_float2(run.exponent, run.sum);
             } else if (MODE == kGrad && (t.product == kHiddenGrad || a.d_w_f32)) {
@@ -690,11 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // bf16: 64 columns are 128 bytes
                 const CUtensorMap *map = MODE == kScore ? &maps.z_out : &maps.dw;
                 const int y = MODE == kScore ? m_first : a.v0 + m_first;
-                // p = 2^(z log2e - lse log2e), the latter as a whole number and the rest: near p = 1 nothing is lost
+                // p = 2^(z log2e - lse log2e), the latter as a whole number and the rest: near p = 1 no more is lost
+                // than lse's own rounding
                 const float whole = rintf(lse * kLog2e), rest = fmaf(lse, kLog2e, -whole);
                 const uint64_t by = f2(kLog2e, kLog2e), less = f2(-whole, -whole), lesser = f2(-rest, -rest), g2 = f2(g, g);
                 uint32_t w[32], rest_w[32];
-                for_blocks(acc, release, [&](uint32_t(&r)[32], int cb) {
+                auto take = [&](uint32_t(&r)[32], int cb) {
                     const int half = cb % 2;
                     if constexpr (MODE == kScore) {
                         const int c = col0 + cb * 32, at = label - c;
@@ -748,7 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             store(w, map, MODE == kScore || x < a.H, x, y, -1, false);
                         }
                     }
-                });
+                };
+                if (MODE == kGrad || group_of(t.stages) == t.stages)
+                    for_blocks(acc, release, take);
+                else if (!for_groups(take))
+                    break;
             }
             t = after;
         }

@@ -376,3 +376,36 @@ def test_few_rows_of_a_large_head(tr, N, H, V):
         b = tr.dflash2_lm_head_loss(bad, W, labels)
         rest = torch.arange(N, device="cuda") != 3
         assert torch.equal(b["lse"][rest], f["lse"][rest]) and torch.equal(b["loss"][rest], f["loss"][rest])
+
+
+@pytest.mark.parametrize("N,H", [(16, 4096), (16, 16384), (128, 4160), (200, 4096), (300, 16384)])
+def test_confident_rows(tr, N, H):
+    """Rows that are nearly fitted: 1 - p of the label from 1e-3 to 1e-5, which is what is left of their gradient.
+
+    The logits of both passes are the same sums, so what they are off by moves every probability by its own share, as
+    other logits would (rel below), and leaves in 1 - p only what lse and exp2 lose: lse's rounding (2^-20 below 32), under
+    40 roundings of 2^-24 of the sum around its largest term, exp2 twice (2^-22), log2(e) as float32 (2^-26 of 32): 2^-17."""
+    V = 2048
+    g = torch.Generator(device="cuda").manual_seed(N + H)
+    W = (randn(g, V, H) / math.sqrt(H)).to(BF16)
+    labels = torch.randint(0, V, (N,), device="cuda", generator=g)
+    top = torch.linspace(math.log(1e3 * V), math.log(1e5 * V), N, device="cuda")[:, None]
+    own = W[labels].float()
+    hidden = (randn(g, N, H) + top * own / own.square().sum(1, keepdim=True)).to(BF16)
+    labels = labels.int()
+    z, lse, _, _ = reference(hidden, W, labels)
+    assert lse.max() < 32
+    f = tr.dflash2_lm_head_loss(hidden, W, labels)
+    got = tr.dflash2_lm_head_loss_grad(hidden, W, labels, f["lse"], torch.ones(N, device="cuda"), d_W=False)["d_hidden"]
+    rows = torch.arange(N, device="cuda")
+    d = torch.exp(z - lse[:, None])
+    d[rows, labels.long()] = 0
+    d[rows, labels.long()] = -d.sum(1)  # p - 1 of the label
+    want = d @ W.double()
+    rel = torch.expm1(2 * logit_error(hidden, W)) + 2.0 ** -16
+    size = W.double().norm(dim=1)
+    parts = (d.abs() * size).sum(1)
+    rounded = (U if N > 128 else U * U) + (V / 8 + 64) * 2.0 ** -23
+    bound = parts * (rel + rounded) + 2.0 ** -17 * size[labels.long()] + U * want.norm(dim=1)
+    off = (got.double() - want).norm(dim=1)
+    assert (off <= bound).all(), (off / bound).max()
