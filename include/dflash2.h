@@ -503,7 +503,7 @@ DF2_API size_t dflash2_lm_head_loss_grad_workspace_bytes(const df2_loss_dims *di
  *   hidden   bf16 [N, H]      W_vocab  bf16 [V, H]
  *   labels   int32 [N]        a row whose label lies outside [0, V) is ignored: its loss is 0
  *   loss     float [N]        lse  float [N], of every row (the gradient takes it)
- * Logits and sums are float32 (tensor cores, bf16 products, at most 1,792 to an accumulator; their sums are added
+ * Logits and sums are float32 (tensor cores, bf16 products, at most 768 to an accumulator; their sums are added
  * rounded to nearest).  A row with a logit that is not finite has an lse
  * that is not (but a logit of -inf counts as exp(-inf) = 0); the other rows are not affected.
  * Limits: 0 <= N <= 2^20, 8 <= H <= 65536 and H % 8 == 0, V < 2^24.  hidden and W_vocab 16-byte aligned.

@@ -409,3 +409,20 @@ def test_confident_rows(tr, N, H):
     bound = parts * (rel + rounded) + 2.0 ** -17 * size[labels.long()] + U * want.norm(dim=1)
     off = (got.double() - want).norm(dim=1)
     assert (off <= bound).all(), (off / bound).max()
+
+
+def test_logits_are_summed_in_groups(tr):
+    """Products that are all positive, so that what an accumulator cuts off adds up: at most 2^-23 of what it holds at each of
+    its steps of 16 products.  It holds a sixteenth of a group's sum on average over the steps of a sixteenth, so a group of
+    768 products loses 24.5 of those at most, its six sums' additions 6 halves more: below 2^-18 of a logit.  One accumulator
+    for all 4096 would lose 128 at most and about half of that."""
+    N, H, V = 20, 4096, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    W = ((0.5 + torch.rand(V, H, device="cuda", generator=g)) / 256).to(BF16)
+    hidden = (0.5 + torch.rand(N, H, device="cuda", generator=g)).to(BF16)
+    labels = torch.arange(N, device="cuda", dtype=torch.int32) % V
+    out = tr.dflash2_lm_head_loss(hidden, W, labels)
+    z, lse, _, _ = reference(hidden, W, labels)
+    # (exp2 and the sum of eight: 2^-22 and 16 roundings of 2^-24; lse's own)
+    bound = z.abs().amax(1) * 2.0 ** -18 + 2.0 ** -20 + lse.abs() * 2.0 ** -23
+    assert ((out["lse"].double() - lse).abs() <= bound).all(), ((out["lse"].double() - lse).abs() / bound).max()
