@@ -266,7 +266,7 @@ struct NormGradArgs {
     const uint4 *z, *gamma, *dy, *d_sum;
     float eps;
     uint4 *dx;
-    float *partial;  // [gridDim.x, C] of dgamma, or null
+    float *partial;  // [gridDim.x, C] of dgamma, 8-byte aligned, or null
 };
 
 // Persistent over rows, so that a thread sums its channels' dgamma in registers.  Each thread copies its own chunks of
@@ -479,7 +479,9 @@ cudaError_t norm_grad(NormGradArgs a, float *dgamma, cudaStream_t stream)
         return e;
     const int resident = std::max(1, std::min({grad_resident(WARP, threads, CHUNKS), kSmem / (smem + 1280), 16}));
     const int parts = std::min({(a.N - 1) / rows + 1, norm_parts(a.C), device_sm_count() * resident});
-    const bool whole = parts == 1;  // one CTA's sums are the result
+    // one CTA's sums are the result, and go there at once if it may be written in pairs (the caller's need not be
+    // aligned to more than a float)
+    const bool whole = parts == 1 && reinterpret_cast<uintptr_t>(dgamma) % 8 == 0;
     if (a.partial && whole)
         a.partial = dgamma;
     e = launch_dependent(kernel, dim3(static_cast<unsigned>(parts)), dim3(threads), smem, stream, a);

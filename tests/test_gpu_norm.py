@@ -269,3 +269,17 @@ def test_two_threads(tr):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not failed
+
+
+@pytest.mark.parametrize("C", [64, 1024, 2048, 16384])
+@pytest.mark.parametrize("N", [1, 2, 5])
+def test_dgamma_anywhere_in_a_flat_buffer(tr, N, C):
+    """A view of a buffer of many gradients, at any element; what lies around it stays."""
+    z, _, gamma = make(N, C, 12)
+    dy = randn(gen(13), N, C).to(BF16)
+    want = tr.dflash2_residual_norm_grad(z, gamma, dy)
+    for at in (1, 2, 3, 4):
+        flat = torch.full((C + 8,), 7.0, device="cuda")
+        got = tr.dflash2_residual_norm_grad(z, gamma, dy, dgamma=flat[at:at + C])
+        assert torch.equal(got["dgamma"], want["dgamma"]) and torch.equal(got["dx"], want["dx"])
+        assert (flat[:at] == 7).all() and (flat[at + C:] == 7).all()
