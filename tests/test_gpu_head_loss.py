@@ -412,10 +412,10 @@ def test_confident_rows(tr, N, H):
 
 
 def test_logits_are_summed_in_groups(tr):
-    """Products that are all positive, so that what an accumulator cuts off adds up: at most 2^-23 of what it holds at each of
-    its steps of 16 products.  It holds a sixteenth of a group's sum on average over the steps of a sixteenth, so a group of
-    768 products loses 24.5 of those at most, its six sums' additions 6 halves more: below 2^-18 of a logit.  One accumulator
-    for all 4096 would lose 128 at most and about half of that."""
+    """Products that are all positive, so that what an accumulator cuts off adds up: at most 2^-23 of what it holds, at each of
+    its steps of 16 products.  A group of 768 takes 48 steps and holds half of its sum on average: it loses 24 times 2^-23 of
+    the sum at most, and the additions of the six sums are rounded, 2^-24 each: below 2^-18 of a logit.  One accumulator for
+    all 4096 loses 128 times 2^-23 at most, and half of that on average (lse was off by twice the bound)."""
     N, H, V = 20, 4096, 8
     g = torch.Generator(device="cuda").manual_seed(3)
     W = ((0.5 + torch.rand(V, H, device="cuda", generator=g)) / 256).to(BF16)
