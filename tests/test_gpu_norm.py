@@ -283,3 +283,28 @@ def test_dgamma_anywhere_in_a_flat_buffer(tr, N, C):
         got = tr.dflash2_residual_norm_grad(z, gamma, dy, dgamma=flat[at:at + C])
         assert torch.equal(got["dgamma"], want["dgamma"]) and torch.equal(got["dx"], want["dx"])
         assert (flat[:at] == 7).all() and (flat[at + C:] == 7).all()
+
+
+def check_gradient(tr, z, gamma, dy, d, eps):
+    out = tr.dflash2_residual_norm_grad(z, gamma, dy, d_sum=d, eps=eps)
+    ds = torch.zeros_like(z, dtype=torch.float64) if d is None else d.double()
+    dx, dg, slack, sums = grad64(z.double(), gamma.double(), dy.double(), ds, eps)
+    close(out["dx"], dx, dx.abs() * U + slack * F + LEAST)
+    close(out["dgamma"], dg, sums * 2.0 ** -16 + 1e-45)
+
+
+@pytest.mark.parametrize("size", [1e-40, 1e-38, 1e-30, 1e-20, 1e19, 1e30, 3e38])
+@pytest.mark.parametrize("C", [64, 1024, 2048, 8192])
+def test_gradient_of_rows_whose_squares_leave_float32(tr, size, C):
+    """dx and dgamma, with eps = 0: 1 / n of a row below the normal range is more than float32 holds, z / n is not."""
+    g = gen(C)
+    z = torch.rand(5, C, device="cuda", generator=g) * 2 - 1
+    z[1:4] *= size
+    z[2, ::3] = 0
+    z, gamma = z.to(BF16), (1 + 0.3 * randn(g, C)).to(BF16)
+    dy, d = (randn(g, 5, C) * 1e-4).to(BF16), randn(g, 5, C).to(BF16)
+    check_gradient(tr, z, gamma, dy, None, 0.0)
+    dy[3] = 0  # nothing came back to this row
+    check_gradient(tr, z, gamma, dy, d, 0.0)
+    out = tr.dflash2_residual_norm_grad(z, gamma, dy, d_sum=d, eps=0.0)
+    assert torch.equal(out["dx"][3], d[3])
