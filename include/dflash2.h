@@ -477,6 +477,7 @@ DF2_API size_t dflash2_residual_norm_grad_workspace_bytes(const df2_norm_dims *d
  *   dx       bf16 [N, C]: the gradient of x and of the residual alike; may be dy or d_sum itself
  *   dgamma   float [C] or NULL (workspace is then not looked at)
  * Limits and alignment as above; an all-zero row with eps = 0 gives dx = d_sum and adds nothing to dgamma.
+ * Rows are scaled as above, so that any finite z is differentiated, with elements of u from 1e-32 to 1e32 or zero.
  * With N = 0 dgamma is zeros.
  */
 DF2_API df2_status dflash2_residual_norm_grad(const df2_norm_dims *dims, const void *z, const void *gamma,

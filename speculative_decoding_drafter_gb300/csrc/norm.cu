@@ -28,6 +28,9 @@ constexpr int kSmem = 227 * 1024; // of an SM
 constexpr float kTiny = 1e-30f;   // a row of codes whose largest magnitude is below this is held as zeros
 // The sum of squares is taken as it is between these; outside, squares may have been lost or overflowed.
 constexpr float kLeast = 1e-24f, kMost = 1e36f;
+// In the gradient it stands next to the sum of u z, which has to hold for any u from 1e-32 to 1e32: a row whose root of
+// the sum is below a thousandth or above a million is brought near one first.
+constexpr float kGradLeast = 1e-6f, kGradMost = 1e12f;
 
 __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, grad_resident(WARP, THREADS, CHUNKS))
         };
         add_up();
         float k = 1.f;
-        if (!(v[0] >= kLeast && v[0] <= kMost)) {  // all threads of a row alike
+        if (!(v[0] >= kGradLeast && v[0] <= kGradMost)) {  // all threads of a row alike
             float m[1] = {0.f};
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {

@@ -308,3 +308,13 @@ def test_gradient_of_rows_whose_squares_leave_float32(tr, size, C):
     check_gradient(tr, z, gamma, dy, d, 0.0)
     out = tr.dflash2_residual_norm_grad(z, gamma, dy, d_sum=d, eps=0.0)
     assert torch.equal(out["dx"][3], d[3])
+
+
+@pytest.mark.parametrize("size,back", [(1e-11, 1e-35), (1e-4, 1e-33), (1e5, 1e30), (1e15, 1e28)])
+@pytest.mark.parametrize("C", [64, 2048, 8192])
+def test_gradient_whose_products_leave_float32(tr, size, back, C):
+    """Rows whose squares float32 holds, and not their products with the gradient."""
+    g = gen(C + 1)
+    z, dy = (randn(g, 3, C) * size).to(BF16), (randn(g, 3, C) * back).to(BF16)
+    dy[1] = z[1] * (back / size)  # along the row: the formula takes most of it away
+    check_gradient(tr, z, (1 + 0.3 * randn(g, C)).to(BF16), dy, None, 0.0)
