@@ -337,20 +337,37 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double *partial, i
         *norm = v;
 }
 
-__device__ __forceinline__ uint32_t scale_word(uint32_t w, int type, float f)
+// What the elements are multiplied by, one after the other.
+struct Factor {
+    float f, by;
+};
+
+// max_norm / total.  A quotient down to 2^-277 is less than float32 holds, or holds in full, and its product with an element may
+// be any number: it goes in two factors, of which the second is a power of two.
+__device__ __forceinline__ Factor factor_of(float max_norm, float total)
 {
-    if (f == 1.f)
+    int e_max, e_total;
+    const float m = frexpf(max_norm, &e_max), t = frexpf(total, &e_total);
+    const int e = e_max - e_total;
+    if (max_norm == 0.f || e >= -120)
+        return Factor{max_norm / total, 1.f};
+    return Factor{ldexpf(m / t, -120), ldexpf(1.f, e + 120)};
+}
+
+__device__ __forceinline__ uint32_t scale_word(uint32_t w, int type, Factor k)
+{
+    if (k.f == 1.f)
         return w;  // a NaN's bits too
     if (type == DF2_F32)
-        return __float_as_uint(__uint_as_float(w) * f);
+        return __float_as_uint(__uint_as_float(w) * k.f * k.by);
     float a, b;
     widen(w, type, a, b);
-    return narrow(a * f, b * f, type);
+    return narrow(a * k.f * k.by, b * k.f * k.by, type);
 }
 
 // From the span's end to its start.
 template <int TYPE>
-__device__ __forceinline__ void scale_span(const Span &s, uint8_t *out, float f)
+__device__ __forceinline__ void scale_span(const Span &s, uint8_t *out, Factor f)
 {
     constexpr int kSize = TYPE == DF2_F32 ? 4 : 2;
     const uint4 *x = reinterpret_cast<const uint4 *>(s.base);
@@ -411,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) scale_kernel(const __gri
         *norm = total;
     // a norm that is not finite leaves the gradients as they are
     const bool over = total > max_norm && total <= 3.4028234e38f;
-    const float f = over ? max_norm / total : 1.f;
+    const Factor f = over ? factor_of(max_norm, total) : Factor{1.f, 1.f};
     int u0, u1;
     share_of(b, u0, u1);
     if (u0 >= u1)

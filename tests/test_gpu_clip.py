@@ -198,3 +198,14 @@ def test_what_is_bound_stays_bound(tr):
     with pytest.raises(ValueError, match="overlap"):
         tr.dflash2_grad_clip([x], norm=x[3:4])
     assert tr.dflash2_grad_clip([x], norm=torch.zeros(1, device="cuda"))["norm"].shape == (1,)
+
+
+@pytest.mark.parametrize("size", [1e-2, 1e20, 1e36])
+@pytest.mark.parametrize("limit", [1.0, 1e-3, 1e-9, 1e-20, 1e-36])
+def test_factors_below_float32(tr, size, limit):
+    """max_norm / norm may be less than float32 holds, what it makes of an element is not."""
+    for apart in (False, True):
+        t = [randn(1, 5001, F32, size), randn(2, 7000, BF16, size), randn(3, 3, F32, size)]
+        check(tr, t, limit, out=[torch.empty_like(x) for x in t] if apart else None)
+        t = [randn(1, 5001, F32, size), randn(2, 7000, BF16, size)]
+        check(tr, t, limit, "max", out=[torch.empty_like(x) for x in t] if apart else None)
