@@ -45,7 +45,7 @@ def _matrix(t, name):
 
 
 def _workspace(nbytes, workspace, device):
-    """(tensor that keeps the scratch alive, address, bytes): 256-byte aligned, not initialised."""
+    """(scratch as a tensor, its address, bytes): 256-byte aligned, not initialised."""
     if workspace is None:
         if nbytes == 0:
             raise ValueError("invalid or unsupported sizes")
@@ -58,7 +58,8 @@ def _workspace(nbytes, workspace, device):
     off = (-workspace.data_ptr()) % 256
     if workspace.numel() - off < nbytes or nbytes == 0:
         raise ValueError(f"workspace must hold {nbytes} bytes from a 256-byte boundary on")
-    return workspace, workspace.data_ptr() + off, nbytes
+    scratch = workspace.view(-1)[off:off + nbytes]
+    return scratch, scratch.data_ptr(), nbytes
 
 
 def _apart(inputs, outputs):
@@ -146,7 +147,7 @@ class ResidualNormGradPlan(_Plan):
                 _ptr(d_sum, BF16, (N, C), "d_sum"), float(eps), _ptr(dx, BF16, (N, C), "dx"),
                 _ptr(dgamma, torch.float32, (C,), "dgamma"), ptr, nbytes)
         _apart([("z", z), ("gamma", gamma), ("dy", dy), ("d_sum", d_sum)],
-               [("dx", dx, ("dy", "d_sum")), ("dgamma", dgamma, ())])
+               [("dx", dx, ("dy", "d_sum")), ("dgamma", dgamma, ()), ("workspace", ws, ())])
         self._bind(args, (dims, z, gamma, dy, d_sum, ws), outputs, stream)
 
 
@@ -213,7 +214,8 @@ class LossPlan(_Plan):
         self.workspace = ws
         args = (_ref(dims), *args, _ptr(loss, torch.float32, (N,), "loss"), _ptr(lse, torch.float32, (N,), "lse"),
                 ws.ptr, ws.nbytes)
-        _apart([("hidden", hidden), ("W_vocab", W_vocab), ("labels", labels)], [("loss", loss, ()), ("lse", lse, ())])
+        _apart([("hidden", hidden), ("W_vocab", W_vocab), ("labels", labels)],
+               [("loss", loss, ()), ("lse", lse, ()), ("workspace", ws.view, ())])
         self._bind(args, (dims, hidden, W_vocab, labels, ws), {"loss": loss, "lse": lse}, stream)
 
 
@@ -240,7 +242,7 @@ class LossGradPlan(_Plan):
                 _ptr(d_W, None if d_W is None else d_W.dtype, (V, H), "d_W"),
                 0 if d_W is None else GRAD_TYPES[d_W.dtype], ws.ptr, ws.nbytes)
         _apart([("hidden", hidden), ("W_vocab", W_vocab), ("labels", labels), ("lse", lse), ("grad", grad)],
-               [("d_hidden", d_hidden, ()), ("d_W", d_W, ())])
+               [("d_hidden", d_hidden, ()), ("d_W", d_W, ()), ("workspace", ws.view, ())])
         outputs = {n: t for n, t in (("d_hidden", d_hidden), ("d_W", d_W)) if t is not None}
         self._bind(args, (dims, hidden, W_vocab, labels, lse, grad, ws), outputs, stream)
 
@@ -304,11 +306,12 @@ class GradClipPlan(_Plan):
         norm = torch.empty((), dtype=torch.float32, device=device) if norm is None else norm
         norm_ptr = _ptr(norm, torch.float32, (1,) if isinstance(norm, torch.Tensor) and norm.dim() else (), "norm")
         spans.append((norm_ptr, norm_ptr + 4, "norm"))
+        ws, ptr, nbytes = _workspace(dflash2_grad_clip_workspace_bytes(len(tensors)), workspace, device)
+        spans.append((ptr, ptr + nbytes, "workspace"))
         spans.sort()
         for a, b in zip(spans, spans[1:]):
             if b[0] < a[1]:
                 raise ValueError(f"{a[2]} and {b[2]} overlap")
-        ws, ptr, nbytes = _workspace(dflash2_grad_clip_workspace_bytes(len(tensors)), workspace, device)
         outputs = {"norm": norm}
         if max_norm is not None:
             outputs["tensors"] = outs

@@ -74,3 +74,39 @@ def test_a_step_captured_follows_its_buffers(example):
 def test_example_runs(example, capsys):
     example.main(["--rows", "64", "--steps", "2"])
     assert "step 1" in capsys.readouterr().out
+
+
+def test_a_workspace_apart_from_what_is_bound():
+    """Scratch that shares memory with a tensor of the call is refused; a part of a larger buffer beside the others is not."""
+    from speculative_decoding_drafter_gb300 import training as tr
+
+    N, C, V = 4, 64, 100
+    n = max(tr.dflash2_residual_norm_grad_workspace_bytes(N, C), tr.dflash2_grad_clip_workspace_bytes(2)) + 256
+    arena = torch.zeros(n + 4096, dtype=torch.uint8, device="cuda")
+    ws, beside = arena[:n], arena[n + (-n) % 256:]
+    z, gamma = torch.ones(N, C, dtype=BF16, device="cuda"), torch.ones(C, dtype=BF16, device="cuda")
+    inside = arena[256:256 + 2 * N * C].view(BF16).view(N, C)
+    for call in (lambda: tr.dflash2_residual_norm_grad(z, gamma, z, dx=inside, workspace=ws),
+                 lambda: tr.dflash2_residual_norm_grad(inside, gamma, z, workspace=ws),
+                 lambda: tr.dflash2_residual_norm_grad(z, gamma, z, dgamma=arena[512:512 + 4 * C].view(torch.float32), workspace=ws),
+                 lambda: tr.dflash2_grad_clip([inside, z], workspace=ws),
+                 lambda: tr.dflash2_grad_clip([z], max_norm=1.0, out=[inside], workspace=ws),
+                 lambda: tr.dflash2_grad_clip([z], norm=arena[256:260].view(torch.float32), workspace=ws)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    dgamma = beside[:4 * C].view(torch.float32)
+    got = tr.dflash2_residual_norm_grad(z, gamma, z, dgamma=dgamma, workspace=ws)
+    assert torch.equal(got["dgamma"], tr.dflash2_residual_norm_grad(z, gamma, z)["dgamma"])
+    assert float(tr.dflash2_grad_clip([dgamma], workspace=ws)["norm"]) == float(tr.dflash2_grad_clip([dgamma])["norm"])
+
+    ids, W = torch.zeros(N, dtype=torch.int32, device="cuda"), torch.zeros(V, C, dtype=BF16, device="cuda")
+    scratch = tr.LossWorkspace(N, C, V)
+    rows = scratch.view[256:256 + 4 * N].view(torch.float32)
+    x = torch.zeros(N, device="cuda")
+    for call in (lambda: tr.dflash2_lm_head_loss(z, W, ids, loss=rows, workspace=scratch),
+                 lambda: tr.dflash2_lm_head_loss(z, W, ids, lse=rows, workspace=scratch),
+                 lambda: tr.dflash2_lm_head_loss_grad(z, W, ids, rows, x, workspace=scratch),
+                 lambda: tr.dflash2_lm_head_loss_grad(z, W, ids, x, x, d_hidden=scratch.view[256:256 + 2 * N * C].view(BF16).view(N, C),
+                                                      workspace=scratch)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
