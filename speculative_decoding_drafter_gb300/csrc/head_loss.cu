@@ -46,6 +46,7 @@
 
 #include "dflash2.h"
 #include "f32x2.cuh"
+#include "head_work.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 #include "tensor_map.h"
@@ -53,11 +54,9 @@
 namespace df2 {
 namespace {
 
-constexpr int kRows = 128;                        // of the accumulator a CTA
-constexpr int kTile = 256;                        // rows and columns of a pair's tile
-constexpr int kBlock = 64;                        // columns of an operand's box: one 128-byte swizzle row
+using namespace head;
+
 constexpr int kBox = kRows * 128;                 // bytes of one block of columns of a box
-constexpr int kStageK = 2 * kBlock;               // elements of K a stage
 constexpr int kStage = 4 * kBox;                  // A's two blocks, B's two blocks
 constexpr int kStages = 3;
 constexpr long long kSpread = 128 << 10, kSpreadFrom = 64 << 20;  // bytes of few rows' copies, and of W that make them
@@ -77,19 +76,12 @@ constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8, kControlRegs = 72, kSumReg
 static_assert(kControlRegs + 2 * kSumRegs <= 3 * kLaunchRegs, "setmaxnreg.inc would wait forever");
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Mode { kLoss = 0, kScore = 1, kGrad = 2 };
-enum Product { kHiddenGrad = 1, kWeightGrad = 2 };  // of a tile; 0: h . W^T
-
-struct Args {
-    int N, H, V;
-    int v0, width;        // the piece's columns: [v0, v0 + width), width a multiple of 256, past V too
-    int row_tiles, col_tiles, h_tiles;
+struct Args : Work {
     int blocks_w;         // whole blocks of 64 columns that W's boxes may be cut from two at a time
     int copies, copy_blocks;  // of the rows side by side, and a copy's blocks of 64 columns (logits; see hidden_copies)
     const int *count;     // rows that are not ignored, packed (null: all N)
     const uint4 *raw;     // the rows as they came, and where the scores' launch puts them for the products (or null)
     uint4 *packed;
-    int parts;            // of dz
     uint16_t *dz;         // [parts, N, pitch of dz] and
     float *sums;          // [splits, parts, N, H], where the epilogue writes few rows itself
     int dz_pitch;
@@ -97,66 +89,9 @@ struct Args {
     const float *lse, *grad;
     float2 *part;         // [2 col_tiles, N] exponent and sum of exponentials (Running)
     float *label_logit;   // [N]
-    // gradient products: tiles of d_hidden first, see tile_of
-    int hidden, weights, splits, first;
-    int hidden_tiles, weight_tiles, early;  // made by the kernel
     int d_w_f32;
     uint32_t *status;
 };
-
-struct Tile {
-    int product;
-    int m0, n0;           // rows of A and of B
-    int k0, stages;       // in stages
-    int split;
-    bool live;
-};
-
-// The pair's i-th tile.
-template <int MODE>
-__device__ __forceinline__ Tile tile_of(const Args &a, int pair, int pairs, int i)
-{
-    Tile t{};
-    if constexpr (MODE != kGrad) {
-        // (counts of tiles fit 32 bits: 16384 rows of the loss at a time, 2^28 elements of dz)
-        const uint32_t u = static_cast<uint32_t>(pair + i * pairs), rows = static_cast<uint32_t>(a.row_tiles);
-        const uint32_t n = u / rows;
-        t.live = n < static_cast<uint32_t>(a.col_tiles);
-        t.m0 = static_cast<int>(u - n * rows) * kTile;
-        t.n0 = static_cast<int>(n) * kTile;
-        t.stages = (a.H + kStageK - 1) / kStageK;
-    } else {
-        // d_hidden's tiles are long and few: they are dealt out first.  Pairs that get one less than the others
-        // work on d_W's tiles meanwhile, for `early` turns, so that all end together.
-        const int rest = a.hidden_tiles % pairs;
-        const int mine = a.hidden_tiles / pairs + (pair < rest ? 1 : 0);
-        const int others = pairs - rest;  // that have one less
-        if (i < mine) {
-            const int j = pair + i * pairs;
-            const int per = a.row_tiles * a.h_tiles, in = j % per;
-            const int ks = a.width / kStageK;
-            t.product = kHiddenGrad;
-            t.live = true;
-            t.split = j / per;
-            t.m0 = in / a.h_tiles * kTile;
-            t.n0 = in % a.h_tiles * kTile;
-            t.k0 = ks * t.split / a.splits;
-            t.stages = ks * (t.split + 1) / a.splits - t.k0;
-        } else {
-            i -= mine;
-            int j = a.early * others + i * pairs + pair;
-            if (pair >= rest)
-                j = i < a.early ? i * others + (pair - rest) : j - a.early * pairs;
-            t.product = kWeightGrad;
-            t.live = j < a.weight_tiles;
-            const int down = static_cast<int>(static_cast<uint32_t>(j) / static_cast<uint32_t>(a.h_tiles));
-            t.m0 = down * kTile;
-            t.n0 = (j - down * a.h_tiles) * kTile;
-            t.stages = max(1, (a.N * a.parts + kStageK - 1) / kStageK);
-        }
-    }
-    return t;
-}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -411,19 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
     Args a = args;
-    if (MODE != kLoss && a.count) {
-        // ignored rows are not there; with none left one tile of zeros makes d_W's
-        a.N = *a.count;
-        a.row_tiles = max(1, (a.N + kTile - 1) / kTile);
-    }
-    if (MODE == kGrad) {
-        a.hidden_tiles = a.hidden ? a.row_tiles * a.h_tiles * a.splits : 0;
-        a.weight_tiles = a.weights ? a.col_tiles * a.h_tiles : 0;
-        // turns of d_W's tiles that take as long as one of d_hidden's: stages, and half of one for a tile's ends
-        a.early = a.hidden_tiles % pairs == 0
-                      ? 0
-                      : max(1, (2 * (a.width / kStageK / a.splits) + 1) / (2 * max(1, (a.N * a.parts + kStageK - 1) / kStageK) + 1));
-    }
+    if (MODE != kLoss && a.count)
+        keep_rows(a, *a.count);  // ignored rows are not there
+    if (MODE == kGrad)
+        share_out(a, pairs);
 
     if (warp < 4) {
         // One place for the whole warpgroup: setmaxnreg wants all its warps at the same instruction, and the
@@ -1068,36 +994,9 @@ cudaError_t launch(const Maps &m, const Args &a, int pairs, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
-
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
-
-LossGradPlan loss_grad_plan(int N, int H, int V)
-{
-    LossGradPlan p;
-    N = std::max(N, 1);
-    // Few rows leave half of a tile's rows, and of a stage's, empty: dz goes there a second time, as what its rounding to bf16
-    // left, and the products are those of float32's dz at nearly the same cost (64 x 5120 x 152064: 804 us,
-    // 783 to 792 without; d_hidden and d_W are off by 1.7e-3, as their own rounding leaves them, instead of 2.1e-3 to 2.6e-3)
-    p.parts = N <= kRows ? 2 : 1;
-    // dz of a piece takes at most half a gigabyte (and the pieces are of one size)
-    const long long most = std::max(1ll, (1ll << 28) / (N * p.parts) / kTile) * kTile;
-    const int pieces = ceil_div(V, most);
-    p.piece = ceil_div(ceil_div(V, pieces), kTile) * kTile;
-    // d_hidden has few tiles where there are few rows: parts of the piece, of two stages at least, are then summed apart, so
-    // that its tiles keep 48 of 76 pairs while the others begin with d_W's (10 x 744 x 114074: 139 us, 152 with tiles for
-    // two turns of all pairs; 254 x 2032 x 18994: 69, 95; 43 x 2792 x 225575: 735, 844).  One row of many tiles is bound by
-    // HBM, which reads and then writes faster than both at once: nearly two turns (16 x 4096 x 151936: 605 us, 634
-    // with 48; 64 x 5120 x 152064: 782, 806 to 823).
-    const int row_tiles = ceil_div(N, kTile), h_tiles = ceil_div(H, kTile);
-    const long long tiles = static_cast<long long>(row_tiles) * h_tiles;
-    const long long most_tiles = row_tiles == 1 && h_tiles >= 12 ? 128 : 48;
-    p.splits = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(p.piece / kStageK / 2), most_tiles / tiles)));
-    p.pitch = ceil_div(H, kBlock) * kBlock;
-    return p;
-}
 
 // Rows that the loss takes at a time: what their tiles leave takes at most 256 MB (or 256 rows).
 static int loss_rows(int N, int V)
@@ -1144,7 +1043,7 @@ struct GradScratch {
 
 static GradScratch carve(int N, int H, int V, void *base)
 {
-    const LossGradPlan p = loss_grad_plan(N, H, V);
+    const GradPlan p = grad_plan(N, H, V);
     const size_t n = static_cast<size_t>(N);
     uint8_t *at = static_cast<uint8_t *>(base);
     size_t off = 0;
@@ -1225,7 +1124,7 @@ cudaError_t launch_lm_head_loss_grad(int N, int H, int V, const void *hidden, co
                                      const float *lse, const float *grad, void *d_hidden, void *d_W, bool d_W_f32,
                                      uint32_t *status, void *scratch, cudaStream_t stream)
 {
-    const LossGradPlan p = loss_grad_plan(N, H, V);
+    const GradPlan p = grad_plan(N, H, V);
     const GradScratch g = carve(N, H, V, scratch);
     // One tile of rows takes the same work with its ignored rows as without: it needs no packing, only zeros in their place,
     // which the scores' launch writes where its boxes can be the caller's rows (a launch less: 3.7 of 20.8 us at

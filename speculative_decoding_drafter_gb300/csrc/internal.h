@@ -196,15 +196,6 @@ cudaError_t launch_residual_norm_grad(int N, int C, const void *z, const void *g
                                       const void *d_sum, float eps, void *dx, float *dgamma, float *partial,
                                       cudaStream_t stream);
 
-// How the gradient of the LM head's loss is cut up, from its sizes alone.
-struct LossGradPlan {
-    int piece;    // columns of the vocabulary at a time, a multiple of 256
-    int splits;   // parts of a piece whose d_hidden is summed apart
-    int pitch;    // elements of a row of the packed hidden states, a multiple of 64
-    int parts;    // bf16 numbers that dz is held in: 2 with few rows
-};
-LossGradPlan loss_grad_plan(int N, int H, int V);
-
 // Scratch behind the status word.
 size_t lm_head_loss_scratch(int N, int H, int V);
 size_t lm_head_loss_grad_scratch(int N, int H, int V);
