@@ -494,7 +494,8 @@ typedef struct df2_loss_dims {
 /* Bytes of workspace of dflash2_lm_head_loss and dflash2_lm_head_loss_grad (0 if dims are out of limits).
  * Each begins with a status word that must be zero before the first call (dflash2_check_device_status
  * reads and clears it); the rest needs no initialisation.  One workspace serves one stream at a time; one
- * that holds the larger of the two serves both calls. */
+ * that holds the larger of the two serves both calls.  Fewer rows may need more (up to 128 rows are held
+ * twice), so a workspace for several sizes holds the largest of their answers. */
 DF2_API size_t dflash2_lm_head_loss_workspace_bytes(const df2_loss_dims *dims);
 DF2_API size_t dflash2_lm_head_loss_grad_workspace_bytes(const df2_loss_dims *dims);
 
@@ -505,8 +506,8 @@ DF2_API size_t dflash2_lm_head_loss_grad_workspace_bytes(const df2_loss_dims *di
  *   labels   int32 [N]        a row whose label lies outside [0, V) is ignored: its loss is 0
  *   loss     float [N]        lse  float [N], of every row (the gradient takes it)
  * Logits and sums are float32 (tensor cores, bf16 products, at most 768 to an accumulator; their sums are added
- * rounded to nearest).  A row with a logit that is not finite has an lse
- * that is not (but a logit of -inf counts as exp(-inf) = 0); the other rows are not affected.
+ * rounded to nearest).  A row with a logit that is not finite, or beyond 2e38, has an lse that is not finite (but a
+ * logit of -inf counts as exp(-inf) = 0); the other rows are not affected.
  * Limits: 0 <= N <= 2^20, 8 <= H <= 65536 and H % 8 == 0, V < 2^24.  hidden and W_vocab 16-byte aligned.
  */
 DF2_API df2_status dflash2_lm_head_loss(const df2_loss_dims *dims, const void *hidden, const void *W_vocab,
@@ -518,9 +519,11 @@ DF2_API df2_status dflash2_lm_head_loss(const df2_loss_dims *dims, const void *h
  *   dz_rv = (exp(z_rv - lse_r) - [v = label_r]) grad_r,  0 in ignored rows
  *   d_hidden bf16 [N, H] = dz . W_vocab   or NULL
  *   d_W      [V, H] = dz^T . hidden, of type d_W_type (DF2_BF16 or DF2_F32), or NULL; at least one of the two
- * The vocabulary is taken in pieces: the logits of a piece are made again, the same bits as the loss's, dz of the piece is rounded to bf16
- * (2^-8 of each at most, as operand of both products; up to 128 rows to the sum of two bf16, 2^-16) and
- * multiplied; sums are float32 and d_hidden and d_W are rounded once.  What an ignored row holds (NaN too) reaches neither; its d_hidden is 0.
+ * The vocabulary is taken in pieces: the logits of a piece are made again, the same bits as the loss's, dz of the
+ * piece is rounded to bf16 (2^-8 of each at most, as operand of both products; up to 128 rows to the sum of two bf16,
+ * 2^-16) and multiplied; sums are float32 (in the tensor cores' accumulators, which cut off: 2^-23 of the sum for
+ * every 16 rows or tokens at most) and d_hidden and d_W are rounded once.  A label's p - 1 is as good as lse, a float32, leaves it.
+ * What an ignored row holds (NaN too) reaches neither; its d_hidden is 0.
  * A row whose lse, grad or hidden is not finite reaches its own d_hidden and all of d_W.
  * Limits and alignment as above; d_hidden and d_W 16-byte aligned and apart from the inputs.  With N = 0 d_W is zeros.
  */

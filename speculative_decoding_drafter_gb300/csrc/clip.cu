@@ -2,11 +2,11 @@
 //
 //   norm = sqrt(sum x^2) or max |x| over every element of every tensor;  out = x min(1, max_norm / norm)
 //
-// HBM-bound: every element is read for the norm, and read and written again for the scaling, which cannot
-// start before the norm is known.  All tensors are one line of units of 16 KB, cut into equal shares, a CTA
-// each, whatever the tensors' sizes; the scaling walks each share from its end, where L2 may still hold what
-// the norm read last.  Two reads and a write of 1.8 GB of bf16: 832 us, 6.5 TB/s; the norm alone of 0.5 GB in 777 tensors 79 us,
-// 6.3 TB/s; of 12 MB in 7 tensors 10.2 us: two launches, each with a chain of arguments -> tensors -> sums.
+// HBM-bound: every element is read for the norm, and read and written again for the scaling, which cannot start
+// before the norm is known.  All tensors are one line of units of 16 KB, cut into equal shares, a CTA each, whatever
+// the tensors' sizes; the scaling walks each share from its end, where L2 may still hold what the norm read last.
+// Two reads and a write of 1.8 GB of bf16: 832 us, 6.5 TB/s; the norm alone of 0.5 GB in 777 tensors 79 us, 6.3 TB/s;
+// of 12 MB in 7 tensors 10.2 us: two launches, each with a chain of arguments -> tensors -> sums.
 //
 // The tensors' addresses and lengths travel in the kernels' arguments (up to 1000 a launch), so a call uploads
 // nothing and leaves no host memory behind that a captured graph would read again.
@@ -174,8 +174,8 @@ __device__ __forceinline__ void share_of(const Batch<M> &b, int &u0, int &u1)
     u1 = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
 }
 
-// ONCE: nobody reads the tensors after, so they need not push others' lines out of L2 (norm of 400 MB beside a cache of written
-// lines: 74 us, 85 otherwise; where they are scaled after, 50 MB take 38 us instead of 31).
+// ONCE: nobody reads the tensors after, so they need not push others' lines out of L2 (norm of 400 MB beside a cache
+// of written lines: 74 us, 85 otherwise; where they are scaled after, 50 MB take 38 us instead of 31).
 template <int TYPE, bool SCALED, bool ONCE>
 __device__ __forceinline__ void add_span(Part &p, const Span &s, float k)
 {
@@ -342,8 +342,8 @@ struct Factor {
     float f, by;
 };
 
-// max_norm / total.  A quotient down to 2^-277 is less than float32 holds, or holds in full, and its product with an element may
-// be any number: it goes in two factors, of which the second is a power of two.
+// max_norm / total.  A quotient down to 2^-277 is less than float32 holds, or holds in full, and its product with an
+// element may be any number: it goes in two factors, of which the second is a power of two.
 __device__ __forceinline__ Factor factor_of(float max_norm, float total)
 {
     int e_max, e_total;
@@ -480,7 +480,8 @@ cudaError_t clip(const df2_tensor *tensors, int n, int kind, float max_norm, boo
     cudaError_t e = cudaSuccess;
     for (int at = 0; at < n; at += M) {
         const int grid = ctas_for(fill(b, tensors, at, n));
-        e = launch_dependent(write ? sum_kernel<M, false> : sum_kernel<M, true>, dim3(grid), dim3(kThreads), 0, stream, b, kind, partial + parts);
+        e = launch_dependent(write ? sum_kernel<M, false> : sum_kernel<M, true>, dim3(grid), dim3(kThreads), 0, stream,
+                             b, kind, partial + parts);
         if (e != cudaSuccess)
             return e;
         parts += grid;
@@ -492,7 +493,8 @@ cudaError_t clip(const df2_tensor *tensors, int n, int kind, float max_norm, boo
     for (int at = (n - 1) / M * M; at >= 0; at -= M) {
         const int grid = ctas_for(fill(b, tensors, at, n));
         e = launch_dependent(scale_kernel<M>, dim3(grid), dim3(kThreads), 0, stream, b, kind, max_norm,
-                             static_cast<const double *>(partial), parts, at == 0 ? norm : static_cast<float *>(nullptr));
+                             static_cast<const double *>(partial), parts,
+                             at == 0 ? norm : static_cast<float *>(nullptr));
         if (e != cudaSuccess)
             return e;
     }

@@ -29,12 +29,13 @@
 //             tiles themselves.
 // Every element is added to by one tile a launch, in the pieces' order: no result depends on which tile is first.
 //
-// What bounds it (one GB300): the products, from about 256 rows on.  Loss of 1024 x 5376 x 262144: 1455-1530 us in short
-// runs, 1.89-1.98 PFLOP/s (cuBLAS's bare bf16 product measured 1.89 to 1.95); 1680-1735 back to back, at the power cap.
-// Gradient of 2048 x 4096 x 151936: 3.80-3.86 ms, 1.98-2.01 PFLOP/s, and 3.98-4.48.  The feed of operands is next: MMAs wait
-// a quarter of their time for boxes in single launches.  Rows of W that do not start on 128-byte lines (H no multiple of
-// 64) are read with a fifth sector in four: 1003 x 1032 x 50021 80 us, 1003 x 1088 72.  Few rows: HBM; loss of 16 x 4096
-// x 151936 200-207 us (6.0-6.2 TB/s), gradient of 64 x 5120 x 152064 804-830 us, of which W read twice and d_W written
+// What bounds it (one GB300): the products, from about 256 rows on.  Loss of 1024 x 5376 x 262144: 1495 us in short
+// runs, 1.93 PFLOP/s (cuBLAS's bare bf16 product measured 1.89 to 1.95); 1674-1744 back to back, at the power cap.
+// Gradient of 2048 x 4096 x 151936 with 1792 rows kept (seven tiles): 3540 us, 1.89 PFLOP/s of the rows kept, and 3985
+// back to back, 1.68; 1794 rows, an eighth tile: 3870 and 4365.  The feed of operands is next: MMAs wait a quarter of
+// their time for boxes in single launches.  Rows of W that do not start on 128-byte lines (H no multiple of 64) are
+// read with a fifth sector in four: 1003 x 1032 x 50021 79 us, 1003 x 1088 72.  Few rows: HBM; loss of 16 x 4096 x
+// 151936 201-207 us (6.0-6.2 TB/s), gradient of 64 x 5120 x 152064 807-835 us, of which W read twice and d_W written
 // take 690.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -71,7 +72,8 @@ constexpr int kStaging = kEpilogue * kWarpBox;
 constexpr int kSmem = 1024 + kStages * kStage + kStaging + kBars;
 static_assert(kSmem <= 227 * 1024, "shared memory of an SM");
 constexpr uint32_t kTmemCols = 512;
-// Registers of the logits' launches: the epilogue holds up to 128 sums a thread and takes what the first four warps need not.
+// Registers of the logits' launches: the epilogue holds up to 128 sums a thread and takes what the first four warps
+// need not.
 constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8, kControlRegs = 72, kSumRegs = 216;
 static_assert(kControlRegs + 2 * kSumRegs <= 3 * kLaunchRegs, "setmaxnreg.inc would wait forever");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -152,8 +154,8 @@ __device__ __forceinline__ RowData row_data(const Args &a, int m)
     return r;
 }
 
-// A running sum of exponentials: sum 2^exponent, the exponent a whole number (so that only the sum is ever rounded), not
-// below the largest logit's.
+// A running sum of exponentials: sum 2^exponent, the exponent a whole number (so that only the sum is ever rounded),
+// not below the largest logit's.
 struct Running {
     float exponent = -INFINITY, sum = 0.f;
 
@@ -183,8 +185,8 @@ struct Running {
     }
 };
 
-// Calls f(columns, block) for each block of 32 columns of a thread's row, the next block on its way from TMEM meanwhile;
-// release() once all have been read.
+// Calls f(columns, block) for each block of 32 columns of a thread's row, the next block on its way from TMEM
+// meanwhile; release() once all have been read.
 template <typename Release, typename F>
 __device__ __forceinline__ void for_blocks(uint32_t acc, Release release, F f)
 {
@@ -206,9 +208,10 @@ __device__ __forceinline__ void for_blocks(uint32_t acc, Release release, F f)
     }
 }
 
-// As for_blocks, with one copy of f in the code and a copy of the registers instead.  The loss alone takes it, whose f is long
-// and stands behind the sums of its groups as well: 16 x 4096 x 151936 199.6 us with it, 205.1 with for_blocks, 1024 x 5376
-// x 262144 1460 and 1475; a head so narrow that the epilogue bounds it loses by it, 1003 x 256 x 50021 32.2 and 30.2.
+// As for_blocks, with one copy of f in the code and a copy of the registers instead.  The loss alone takes it, whose
+// f is long and stands behind the sums of its groups as well: 16 x 4096 x 151936 205 us with it, 210 with for_blocks,
+// 1024 x 5376 x 262144 1497 and 1507; a head so narrow that the epilogue bounds it loses by it, 1003 x 256 x 50021
+// 31.9 and 29.9.
 template <typename Release, typename F>
 __device__ __forceinline__ void for_blocks_once(uint32_t acc, Release release, F f)
 {
@@ -264,13 +267,14 @@ __device__ __forceinline__ void stage_row(uint32_t buf, int lane, const uint32_t
                      : "memory");
 }
 
-// Logits of many products: the stages are cut into even groups, whose sums the epilogue adds up rounded to nearest.  An
-// accumulator cuts off what does not fit (256 times for 4096 products: lse is then off by 1.8e-6 of it).  Groups of at most
-// 6 stages leave 5.7e-7 in the worst of a dozen sizes, of 14 1.4e-6, of 4 3.9e-7; 1024 x 5376 x 262144 takes 1484 us with
-// 6, 1486 to 1500 with 14, 1495 with 4; 1003 x 1024 x 50021 66.2, 65.9, 66.5.  The gradient's logits are the same sums, bit by
-// bit: what a label's logit is off by is then in its row's lse too, and 1 - p of a row that is nearly fitted keeps its value
-// (1 - p near 1e-5, H = 4096: d_hidden off by 5% in the median, 20% and up to 47 times with all of H in one accumulator, which
-// cuts off more than lse's groups did; 64 x 5120 x 152064 takes 818 us and 816).
+// Logits of many products: the stages are cut into even groups, whose sums the epilogue adds up rounded to nearest.
+// An accumulator cuts off what does not fit (256 times for 4096 products: lse is then off by 1.8e-6 of it).  Groups
+// of at most 6 stages leave 5.7e-7 in the worst of a dozen sizes, of 14 1.4e-6, of 4 3.9e-7; 1024 x 5376 x 262144
+// takes 1484 us with 6, 1486 to 1500 with 14, 1495 with 4; 1003 x 1024 x 50021 66.2, 65.9, 66.5. The gradient's
+// logits are the same sums, bit by bit: what a label's logit is off by is then in its row's lse too, and 1 - p of a
+// row that is nearly fitted keeps its value (1 - p from 2e-6 to 1e-3, H = 4096: the worst row's d_hidden is off by 5
+// to 15%, which is lse's own rounding; by 21 to 47 times its size if the gradient's logits had one accumulator.  64 x
+// 5120 x 152064 takes 0.4% more with groups).
 __device__ __forceinline__ int group_of(int stages)
 {
     const int groups = (stages + kGroup - 1) / kGroup;
@@ -498,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         if (MODE == kScore && a.raw) {
-            // under the first tile's products: ignored rows become zeros, for what they hold must not reach d_W (0 . NaN)
+            // under the first tile's products: ignored rows become zeros, for what they hold must not reach d_W (0 .
+            // NaN)
             const int chunks = a.H / 8, total = a.N * chunks;
             for (int i = blockIdx.x * 32 * kEpilogue + threadIdx.x - 128; i < total; i += gridDim.x * 32 * kEpilogue) {
                 const int label = a.labels[i / chunks];
@@ -551,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t = after;
                 continue;
             }
-            // The logits of a tile of several groups (this one's accumulator is the first's): their sums, block by block, to f.
-            // False if an accumulator does not come.
+            // The logits of a tile of several groups (this one's accumulator is the first's): their sums, block by
+            // block, to f. False if an accumulator does not come.
             auto for_groups = [&](auto f) {
                 uint32_t sum[kCols / 32][32] = {};
                 const int group = group_of(t.stages);
@@ -612,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int x = n_first + cb * 32;
                     if (two && a.first) {
                         if (y + lane < a.N)
-                            store_row(a.sums + (static_cast<long long>(z) * a.N + y + lane) * a.H + x, (a.H - x) / 8, r);
+                            store_row(a.sums + (static_cast<long long>(z) * a.N + y + lane) * a.H + x, (a.H - x) / 8,
+                                      r);
                     } else {
                         store(r, map, x < a.H, x, y, z, !a.first);
                     }
@@ -624,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // p = 2^(z log2e - lse log2e), the latter as a whole number and the rest: near p = 1 no more is lost
                 // than lse's own rounding
                 const float whole = rintf(lse * kLog2e), rest = fmaf(lse, kLog2e, -whole);
-                const uint64_t by = f2(kLog2e, kLog2e), less = f2(-whole, -whole), lesser = f2(-rest, -rest), g2 = f2(g, g);
+                const uint64_t by = f2(kLog2e, kLog2e), less = f2(-whole, -whole), lesser = f2(-rest, -rest);
+                const uint64_t g2 = f2(g, g);
                 uint32_t w[32], rest_w[32];
                 auto take = [&](uint32_t(&r)[32], int cb) {
                     const int half = cb % 2;
@@ -669,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (half) {
                         const int x = n_first + (cb - 1) * 32;
                         if (MODE == kScore && a.parts == 2) {
-                            // few rows: each lane's by itself, without waiting for a staging buffer to be read (8 x 256 x
-                            // 4096: 16.9 us, 17.5 through staging)
+                            // few rows: each lane's by itself, without waiting for a staging buffer to be read (8 x
+                            // 256 x 4096: 16.9 us, 17.5 through staging)
                             if (m < a.N) {
                                 uint16_t *to = a.dz + static_cast<long long>(m) * a.dz_pitch + x;
                                 store_row(to, 4, w);
@@ -755,9 +762,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(const float2 *part, int tile
     }
 }
 
-// Rows of H elements, a multiple of 8, as rows of `pitch`, a multiple of 64: boxes of rows that start on a 128-byte line each
-// are read from L2 without a fifth sector in four.  With labels, ignored rows become zeros (what they hold must not
-// reach a product: 0 . NaN); the whole is written `times` times, `step` chunks apart, rows `row_step`.
+// Rows of H elements, a multiple of 8, as rows of `pitch`, a multiple of 64: boxes of rows that start on a 128-byte
+// line each are read from L2 without a fifth sector in four.  With labels, ignored rows become zeros (what they hold
+// must not reach a product: 0 . NaN); the whole is written `times` times, `step` chunks apart, rows `row_step`.
 __global__ void __launch_bounds__(256) pad_kernel(const uint4 *hidden, const int32_t *labels, int N, int V, int whole,
                                                   int chunks, int times, long long step, int row_step, uint4 *padded)
 {
@@ -837,14 +844,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint4 *hidden, const in
     if (r1 == N) {
         if (threadIdx.x == 0)
             *p.count = before;
-        const long long end = static_cast<long long>(min(N, (max(before, 1) + kStageK - 1) / kStageK * kStageK)) * chunks;
+        const int padded = min(N, (max(before, 1) + kStageK - 1) / kStageK * kStageK);
+        const long long end = static_cast<long long>(padded) * chunks;
         for (long long c = static_cast<long long>(before) * chunks + threadIdx.x; c < end; c += 256)
             p.hidden[c] = make_uint4(0, 0, 0, 0);
     }
 }
 
-// d_hidden = the sums of the splits and of dz's parts, rounded; zeros for ignored rows.  place: where a row's sums are (null: in
-// its own place).  GROUP threads share eight elements, where many sums are read for few of them.
+// d_hidden = the sums of the splits and of dz's parts, rounded; zeros for ignored rows.  place: where a row's sums
+// are (null: in its own place).  GROUP threads share eight elements, where many sums are read for few of them.
 template <int GROUP>
 __global__ void __launch_bounds__(256) hidden_grad_kernel(const float4 *sums, int count, int N, int chunks,
                                                           const int32_t *place, const int32_t *labels, int V,
@@ -872,7 +880,8 @@ __global__ void __launch_bounds__(256) hidden_grad_kernel(const float4 *sums, in
         for (int d = GROUP / 2; d > 0; d /= 2)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[j] += __shfl_xor_sync(GROUP == 1 ? 0xffffffffu : ((1u << GROUP) - 1u) << (threadIdx.x % 32 / GROUP * GROUP), x[j], d);
+                x[j] += __shfl_xor_sync(
+                    GROUP == 1 ? 0xffffffffu : ((1u << GROUP) - 1u) << (threadIdx.x % 32 / GROUP * GROUP), x[j], d);
         if (g == 0)
             d_hidden[i] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
     }
@@ -898,8 +907,8 @@ cudaError_t load_map(CUtensorMap *map, const void *p, long long rows, int cols, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Both maps of a matrix, and how many blocks load_box may take from the first (with columns that are a multiple of 64 that
-// is any: past the end it reads zeros).
+// Both maps of a matrix, and how many blocks load_box may take from the first (with columns that are a multiple of 64
+// that is any: past the end it reads zeros).
 cudaError_t load_maps(CUtensorMap *map, CUtensorMap *tail, int *blocks, const void *p, long long rows, int cols)
 {
     *blocks = cols % kBlock == 0 ? 1 << 30 : cols / kBlock;
@@ -1005,11 +1014,12 @@ static int loss_rows(int N, int V)
     return static_cast<int>(std::min<long long>(N, std::max(1ll * kTile, std::min(16384ll, rows))));
 }
 
-// Copies of few rows that the logits' launch reads, each pair of CTAs one of them: all pairs read all rows while W streams by,
-// and that is slow where the rows lie in less than 128 KB, by how their address falls (they are then few slices of L2's work):
-// loss of 1 x 4096 x 151936 207 us, 293 to 390 without copies; 8 rows 207, 240 to 332; 1 x 4560 x 223738 341, 549; with
-// 64 KB 288, 236 and 403.  16 rows, 128 KB, take 206 wherever they lie.  The launch that makes the copies costs more than it
-// gives for a small W (41 MB: 18.4 to 20 us, 17.8 to 19.4 without; 131 MB: 34 to 36, 40 to 47).
+// Copies of few rows that the logits' launch reads, each pair of CTAs one of them: all pairs read all rows while W
+// streams by, and that is slow where the rows lie in less than 128 KB, by how their address falls (they are then few
+// slices of L2's work): loss of 1 x 4096 x 151936 207 us, 293 to 390 without copies; 8 rows 207, 240 to 332; 1 x 4560
+// x 223738 341, 549; with 64 KB 288, 236 and 403.  16 rows, 128 KB, take 206 wherever they lie.  The launch that
+// makes the copies costs more than it gives for a small W (41 MB: 18.4 to 20 us, 17.8 to 19.4 without; 131 MB: 34 to
+// 36, 40 to 47).
 static int hidden_copies(int N, int H, int V)
 {
     const long long bytes = static_cast<long long>(N) * ceil_div(H, kStageK) * kStageK * 2;
@@ -1086,7 +1096,8 @@ cudaError_t launch_lm_head_loss(int N, int H, int V, const void *hidden, const v
     uint4 *const padded = pitch ? reinterpret_cast<uint4 *>(at) : nullptr;
     at += round256(static_cast<size_t>(rows) * a.copies * pitch * 2);
     a.part = reinterpret_cast<float2 *>(at);
-    a.label_logit = reinterpret_cast<float *>(at + round256(static_cast<size_t>(rows) * 2 * a.col_tiles * sizeof(float2)));
+    at += round256(static_cast<size_t>(rows) * 2 * a.col_tiles * sizeof(float2));
+    a.label_logit = reinterpret_cast<float *>(at);
     cudaError_t e = load_maps(&m.w, &m.w_tail, &a.blocks_w, W, V, H);
     if (e != cudaSuccess)
         return e;
@@ -1098,9 +1109,9 @@ cudaError_t launch_lm_head_loss(int N, int H, int V, const void *hidden, const v
         if (padded) {
             const long long chunks = static_cast<long long>(a.N) * (pitch / 8);
             e = launch_dependent(pad_kernel, dim3(static_cast<unsigned>(std::min(1216ll, (chunks + 255) / 256))),
-                                 dim3(256), 0, stream, reinterpret_cast<const uint4 *>(h), static_cast<const int32_t *>(nullptr),
-                                 a.N, V, H / 8, pitch / 8, a.copies, static_cast<long long>(pitch / 8),
-                             a.copies * (pitch / 8), padded);
+                                 dim3(256), 0, stream, reinterpret_cast<const uint4 *>(h),
+                                 static_cast<const int32_t *>(nullptr), a.N, V, H / 8, pitch / 8, a.copies,
+                                 static_cast<long long>(pitch / 8), a.copies * (pitch / 8), padded);
             if (e != cudaSuccess)
                 return e;
             h = reinterpret_cast<const uint16_t *>(padded);
@@ -1126,9 +1137,9 @@ cudaError_t launch_lm_head_loss_grad(int N, int H, int V, const void *hidden, co
 {
     const GradPlan p = grad_plan(N, H, V);
     const GradScratch g = carve(N, H, V, scratch);
-    // One tile of rows takes the same work with its ignored rows as without: it needs no packing, only zeros in their place,
-    // which the scores' launch writes where its boxes can be the caller's rows (a launch less: 3.7 of 20.8 us at
-    // 8 x 256 x 4096).
+    // One tile of rows takes the same work with its ignored rows as without: it needs no packing, only zeros in their
+    // place, which the scores' launch writes where its boxes can be the caller's rows (a launch less: 3.7 of 20.8 us
+    // at 8 x 256 x 4096).
     const bool in_place = N <= kTile && H % kBlock == 0, few = in_place || p.parts == 2;
     cudaError_t e = cudaSuccess;
     if (!few) {
@@ -1142,10 +1153,13 @@ cudaError_t launch_lm_head_loss_grad(int N, int H, int V, const void *hidden, co
                              p.pitch / 8, g.packed.hidden);
     }
     const int copies = hidden_copies(N, H, V), copied = copied_pitch(N, H, V);
-    if (e == cudaSuccess && copies > 1)  // (few rows)
-        e = launch_dependent(pad_kernel, dim3(static_cast<unsigned>(ceil_div(static_cast<long long>(N) * (copied / 8), 256))),
-                             dim3(256), 0, stream, static_cast<const uint4 *>(hidden), labels, N, V, H / 8, copied / 8, copies,
-                             static_cast<long long>(copied / 8), copies * (copied / 8), g.copies);
+    if (e == cudaSuccess && copies > 1) {  // (few rows)
+        const int chunks = copied / 8;
+        e = launch_dependent(pad_kernel,
+                             dim3(static_cast<unsigned>(ceil_div(static_cast<long long>(N) * chunks, 256))), dim3(256),
+                             0, stream, static_cast<const uint4 *>(hidden), labels, N, V, H / 8, chunks, copies,
+                             static_cast<long long>(chunks), copies * chunks, g.copies);
+    }
     if (e != cudaSuccess)
         return e;
     Maps m{};

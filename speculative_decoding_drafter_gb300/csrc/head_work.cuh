@@ -1,5 +1,5 @@
-// head_work.cuh -- how the LM-head loss's products are cut into tiles and dealt out to the pairs of CTAs.  Arithmetic alone,
-// so that a test can compile it for the host and follow every pair's share.
+// head_work.cuh -- how the LM-head loss's products are cut into tiles and dealt out to the pairs of CTAs.  Arithmetic
+// alone, so that a test can compile it for the host and follow every pair's share.
 #pragma once
 
 #include <algorithm>
@@ -52,8 +52,8 @@ DF2_HEAD_WORK void keep_rows(Work &a, int n)
     a.row_tiles = larger(1, (n + kTile - 1) / kTile);
 }
 
-// The gradient's tiles, and how many turns of d_W's tiles take as long as one of d_hidden's: stages, and half of one for a
-// tile's ends.
+// The gradient's tiles, and how many turns of d_W's tiles take as long as one of d_hidden's: stages, and half of one
+// for a tile's ends.
 DF2_HEAD_WORK void share_out(Work &a, int pairs)
 {
     a.hidden_tiles = a.hidden ? a.row_tiles * a.h_tiles * a.splits : 0;
@@ -121,23 +121,24 @@ inline GradPlan grad_plan(int N, int H, int V)
 {
     GradPlan p;
     N = larger(N, 1);
-    // Few rows leave half of a tile's rows, and of a stage's, empty: dz goes there a second time, as what its rounding to bf16
-    // left, and the products are those of float32's dz at nearly the same cost (64 x 5120 x 152064: 804 us,
-    // 783 to 792 without; d_hidden and d_W are off by 1.7e-3, as their own rounding leaves them, instead of 2.1e-3 to 2.6e-3)
+    // Few rows leave half of a tile's rows, and of a stage's, empty: dz goes there a second time, as what its rounding to
+    // bf16 left, and the products are those of float32's dz at nearly the same cost (64 x 5120 x 152064: 807 us, 778
+    // without; d_hidden and d_W are off by 1.7e-3, as their own rounding leaves them, instead of 2.1e-3 to 2.6e-3)
     p.parts = N <= kRows ? 2 : 1;
     // dz of a piece takes at most half a gigabyte (and the pieces are of one size)
     const long long most = std::max(1ll, (1ll << 28) / (N * p.parts) / kTile) * kTile;
     const int pieces = ceil_div(V, most);
     p.piece = ceil_div(ceil_div(V, pieces), kTile) * kTile;
-    // d_hidden has few tiles where there are few rows: parts of the piece, of two stages at least, are then summed apart, so
-    // that its tiles keep 48 of 76 pairs while the others begin with d_W's (10 x 744 x 114074: 139 us, 152 with tiles for
-    // two turns of all pairs; 254 x 2032 x 18994: 69, 95; 43 x 2792 x 225575: 735, 844).  One row of many tiles is bound by
-    // HBM, which reads and then writes faster than both at once: nearly two turns (16 x 4096 x 151936: 605 us, 634
-    // with 48; 64 x 5120 x 152064: 782, 806 to 823).
+    // d_hidden has few tiles where there are few rows: parts of the piece, of two stages at least, are then summed apart,
+    // so that its tiles keep 48 of 76 pairs while the others begin with d_W's (10 x 744 x 114074: 128 us, 132 with tiles
+    // for two turns of all pairs; 254 x 2032 x 18994: 72, 82; 43 x 2792 x 225575: 755, 804).  One row of many tiles is
+    // bound by HBM, which reads and then writes faster than both at once: nearly two turns (16 x 4096 x 151936: 617 us,
+    // 641 with 48; 64 x 5120 x 152064: 807, 820).
     const int row_tiles = ceil_div(N, kTile), h_tiles = ceil_div(H, kTile);
     const long long tiles = static_cast<long long>(row_tiles) * h_tiles;
     const long long most_tiles = row_tiles == 1 && h_tiles >= 12 ? 128 : 48;
-    p.splits = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(p.piece / kStageK / 2), most_tiles / tiles)));
+    const long long most_parts = std::min(static_cast<long long>(p.piece / kStageK / 2), most_tiles / tiles);
+    p.splits = static_cast<int>(std::max(1ll, most_parts));
     p.pitch = ceil_div(H, kBlock) * kBlock;
     return p;
 }

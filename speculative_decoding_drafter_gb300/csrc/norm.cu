@@ -92,8 +92,8 @@ struct Max {
     __device__ static float apply(float a, float b) { return a > b || a != a ? a : b; }
 };
 
-// The N values of each thread reduced over the threads of a row (WARP: a warp, otherwise the CTA), in one
-// order; every thread gets them.  `slots` holds two turns of kMaxWarps values for each of MOST, the most that the kernel
+// The N values of each thread reduced over the threads of a row (WARP: a warp, otherwise the CTA), in one order;
+// every thread gets them.  `slots` holds two turns of kMaxWarps values for each of MOST, the most that the kernel
 // reduces at once; `turn` tells a call's from the one's before, whose values another warp may still be reading.
 template <bool WARP, typename Op, int MOST, int N>
 __device__ __forceinline__ void row_reduce(float (&v)[N], float *slots, int &turn)
@@ -264,12 +264,12 @@ struct NormGradArgs {
     float *partial;  // [gridDim.x, C] of dgamma, 8-byte aligned, or null
 };
 
-// Persistent over rows, so that a thread sums its channels' dgamma in registers.  Each thread copies its own chunks of
-// the next DEPTH - 1 rows into shared memory (cp.async: no registers, and nothing to wait for but its own copies): the
-// loads of one row would leave HBM idle while the row is reduced (8195 x 5120: 70.4 us without, 56.3 now, 5.97 TB/s; 40
-// instructions an element bound it then, hence pairs of float32).  160 threads with four chunks instead of 320 with two: 95 us.
-// CTAs of the gradient that an SM holds at once, as far as registers go: a thread of four chunks takes up to 128, of two
-// or one 64 (80 where a row is a warp's).
+// Persistent over rows, so that a thread sums its channels' dgamma in registers.  Each thread copies its own chunks
+// of the next DEPTH - 1 rows into shared memory (cp.async: no registers, and nothing to wait for but its own copies):
+// the loads of one row would leave HBM idle while the row is reduced (8195 x 5120: 70.4 us without, 56.3 now, 5.97
+// TB/s; 40 instructions an element bound it then, hence pairs of float32).  160 threads with four chunks instead of
+// 320 with two: 95 us. CTAs of the gradient that an SM holds at once, as far as registers go: a thread of four chunks
+// takes up to 128, of two or one 64 (80 where a row is a warp's).
 __host__ __device__ constexpr int grad_resident(bool warp, int threads, int chunks)
 {
     return warp ? (chunks == 4 ? 512 : 768) / threads : 1024 / threads;
@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(THREADS, grad_resident(WARP, THREADS, CHUNKS))
         const float inv = under == 0.f ? 0.f : rsqrtf(under);  // 1 / (n k)
         const float back = v[1] * inv_C * inv;                 // mean(u z / n)
         const uint64_t inv2 = f2(inv, inv), back2 = f2(-back, -back);
-        // (1 / n of a row below float32's normal range is more than float32 holds: 1 / (n k) and k come one after the other.
-        // The loop twice, because every instruction of it counts: 0 to 0.7% slower than one that could not do this, 2 to 7% up
-        // to 512 channels; k where each element is finished costs 12% at 16384 x 4096.)
+        // (1 / n of a row below float32's normal range is more than float32 holds: 1 / (n k) and k come one after the
+        // other. The loop twice, because every instruction of it counts: 0 to 0.7% slower than one that could not do
+        // this, 2 to 7% up to 512 channels; k where each element is finished costs 12% at 16384 x 4096.)
         auto finish = [&](auto scaled) {
             const uint64_t k2 = f2(k, k);
 #pragma unroll
@@ -565,8 +565,8 @@ cudaError_t launch_residual_norm_grad(int N, int C, const void *z, const void *g
         return norm_grad<true, 128, 2, 4>(a, dgamma, stream);
     if (C <= 1024)
         return norm_grad<true, 128, 4, 3>(a, dgamma, stream);
-    // places for as many rows of a CTA's as let two CTAs share an SM (16384 x 4096: 87 us with four, 99 with three; 8195 x 5120:
-    // 56.3 us with three, 59.0 with two, 74.1 with four, which leave room for one CTA)
+    // places for as many rows of a CTA's as let two CTAs share an SM (16384 x 4096: 87 us with four, 99 with three;
+    // 8195 x 5120: 56.3 us with three, 59.0 with two, 74.1 with four, which leave room for one CTA)
     const int threads = threads_for(C, 2);
     if (threads <= 256)
         return norm_grad<false, 256, 2, 4>(a, dgamma, stream);

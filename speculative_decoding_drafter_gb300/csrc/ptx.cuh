@@ -396,7 +396,10 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 }
 
 // The same where nothing that this thread wrote to memory has to be seen by who waits (a release of the cluster's
-// scope waits for the thread's own stores, about 1,500 cycles on GB300).
+// scope waits for the thread's own stores, about 1,500 cycles on GB300).  It lets go of an accumulator that was read:
+// tcgen05.wait::ld has brought the values into registers before, so that no later product can change them, and
+// tcgen05.fence::before_thread_sync here and fence::after_thread_sync behind the wait order the reads before those
+// products; both fences order against the arrival and the wait as execution, which needs no release of memory.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

@@ -165,7 +165,8 @@ def dflash2_lm_head_loss_grad_workspace_bytes(N: int, H: int, V: int) -> int:
 
 class LossWorkspace:
     """Device scratch of dflash2_lm_head_loss and, with `grad`, of dflash2_lm_head_loss_grad too (256-byte aligned, its
-    status word zeroed on the current stream when allocated); dflash2_check_device_status takes it."""
+    status word zeroed on the current stream when allocated); dflash2_check_device_status takes it.  It serves other
+    sizes that need no more (fewer rows may: up to 128 are held twice)."""
 
     def __init__(self, N: int, H: int, V: int, *, grad: bool = True, device=None):
         n = dflash2_lm_head_loss_workspace_bytes(N, H, V)
