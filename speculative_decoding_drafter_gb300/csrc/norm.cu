@@ -268,8 +268,10 @@ struct NormGradArgs {
 // of the next DEPTH - 1 rows into shared memory (cp.async: no registers, and nothing to wait for but its own copies):
 // the loads of one row would leave HBM idle while the row is reduced (8195 x 5120: 70.4 us without, 56.3 now, 5.97
 // TB/s; 40 instructions an element bound it then, hence pairs of float32).  160 threads with four chunks instead of
-// 320 with two: 95 us. CTAs of the gradient that an SM holds at once, as far as registers go: a thread of four chunks
-// takes up to 128, of two or one 64 (80 where a row is a warp's).
+// 320 with two: 95 us.
+
+// CTAs of the gradient that an SM holds at once, as far as registers go: a thread of four chunks takes up to 128, of
+// two or one 64 (80 where a row is a warp's).
 __host__ __device__ constexpr int grad_resident(bool warp, int threads, int chunks)
 {
     return warp ? (chunks == 4 ? 512 : 768) / threads : 1024 / threads;
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, grad_resident(WARP, THREADS, CHUNKS))
         const float back = v[1] * inv_C * inv;                 // mean(u z / n)
         const uint64_t inv2 = f2(inv, inv), back2 = f2(-back, -back);
         // (1 / n of a row below float32's normal range is more than float32 holds: 1 / (n k) and k come one after the
-        // other. The loop twice, because every instruction of it counts: 0 to 0.7% slower than one that could not do
+        // other.  The loop twice, because every instruction of it counts: 0 to 0.7% slower than one that could not do
         // this, 2 to 7% up to 512 channels; k where each element is finished costs 12% at 16384 x 4096.)
         auto finish = [&](auto scaled) {
             const uint64_t k2 = f2(k, k);
